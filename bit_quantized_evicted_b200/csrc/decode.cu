@@ -85,9 +85,50 @@ constexpr int kOffKc = 0, kOffVc = 1024, kOffKs = 2048, kOffKz = 2304, kOffVs = 
 constexpr int kOffRk = 0, kOffRv = kResTok * 256;
 static_assert(2 * kResTok * 256 <= kStageBytes, "residual item fits a stage");
 
+// Windowed calls (minikv_decode_attn_window): what sequence b hides this step.
+// Its n_all packed and r_all residual tokens (the new one included) are
+// numbered in order of arrival; those in [n_sink, n - window) are hidden.
+// Whole hidden slices and a hidden run at the start of the residual take no
+// part in the work list: the lengths the list is built from (s_nq, s_r, s_rs)
+// count what is left, and packed item j stands for slice j + gap from slice
+// gap0 on.  Hidden tokens inside a listed slice (packed tokens [ph0, ph1)) or
+// residual item (listed residual tokens [rh0, rh1): only where the sinks reach
+// into the residual) are masked.
+struct WinSeq {
+    int nq, r, rs;             // what the work list sees
+    int n_all, r_all, rs_all;  // the sequence's own state (flush, next state)
+    int gap0, gap, ph0, ph1, rh0, rh1;
+};
+__host__ __device__ __forceinline__ WinSeq win_seq(int nq, int r, int rs, int ring, int window, int n_sink) {
+    WinSeq w;
+    w.n_all = nq;
+    w.r_all = r;
+    w.rs_all = rs;
+    const int n = nq + r;
+    const int lo = n > window ? n - window : 0;       // first token of the window
+    const int ns = n_sink < lo ? n_sink : lo;         // sinks before it
+    w.ph0 = ns;
+    w.ph1 = lo;
+    w.gap0 = (ns + kSlice - 1) / kSlice;
+    const int g1 = (lo < nq ? lo : nq) / kSlice;
+    w.gap = g1 > w.gap0 ? g1 - w.gap0 : 0;
+    const int r0 = ns <= nq && lo > nq ? lo - nq : 0;   // < r: the new token is always in the window
+    w.nq = nq - w.gap * kSlice;
+    w.r = r - r0;
+    w.rs = rs + r0 >= ring ? rs + r0 - ring : rs + r0;
+    w.rh0 = ns - (nq + r0);
+    w.rh1 = lo - (nq + r0);
+    if (w.rh0 < 0) w.rh0 = w.rh1 = 0;                   // r0 took the hidden run, or there is none
+    return w;
+}
+
 // One unit's share of a CTA's range ("segment").
 struct Seg {
     int u, b, ub, items, nri, nq, r, rs, first, S_u, hi;
+};
+// ... of a windowed call
+struct SegWin : Seg {
+    WinSeq w;
 };
 
 struct __align__(16) Smem {
@@ -98,10 +139,12 @@ struct __align__(16) Smem {
     uint4 zero;
     int flag;
     int next;   // next item of the CTA's range to claim
-    Seg seg;    // the unit being processed
+    SegWin seg;   // the unit being processed
 };
 
 struct Args {
+    static constexpr bool kWin = false;   // windowed call
+    static constexpr bool kPre = false;   // the batch also attends to a shared prefix
     const uint32_t *k_codes, *v_codes;
     const uint16_t *k_scale, *k_zero, *v_scale, *v_zero;
     uint32_t *k_codes_w, *v_codes_w;
@@ -194,7 +237,9 @@ __device__ __forceinline__ int part_P(const ArgsVar &a) { return a.P; }
 
 // Device-state mode: the table sits behind Smem in dynamic shared memory:
 // DevTab, then n_q[B], r[B], res_start[B], ibeg[B + 1], cta_lo[P + 1],
-// status[B] (int; P = the launch's partition bound a.P).
+// status[B] (int; P = the launch's partition bound a.P), and in windowed calls
+// the sequences' own n_q[B], r[B], res_start[B] (the first three then hold
+// what the work list sees).
 struct ArgsDev : Args {};
 struct DevTab {
     long long Wt;
@@ -219,6 +264,27 @@ __device__ __forceinline__ int seq_of_x(const ArgsDev &a, int x) {
 }
 __device__ __forceinline__ int cta_lo(const ArgsDev &a, int c) { return dev_arr(a, 4)[c]; }
 __device__ __forceinline__ int part_P(const ArgsDev &) { return dev_tab().P; }
+// the sequences' own state in a windowed call: k = 0 n_q, 1 r, 2 res_start
+__device__ __forceinline__ int *dev_own(const Args &a, int k) { return dev_arr(a, 4) + a.P + 1 + (k + 1) * nseq(a); }
+
+// ---- windowed calls: each mode's arguments with the window, and sequence b's record
+struct ArgsUniWin : ArgsUni {
+    static constexpr bool kWin = true;
+    WinSeq win;
+};
+struct ArgsVarWin : ArgsVar {
+    static constexpr bool kWin = true;
+    WinSeq win[kMaxRaggedSeqs];
+};
+struct ArgsDevWin : ArgsDev {
+    static constexpr bool kWin = true;
+    int window, n_sink;
+};
+__device__ __forceinline__ WinSeq s_win(const ArgsUniWin &a, int) { return a.win; }
+__device__ __forceinline__ WinSeq s_win(const ArgsVarWin &a, int b) { return a.win[b]; }
+__device__ __forceinline__ WinSeq s_win(const ArgsDevWin &a, int b) {
+    return win_seq(dev_own(a, 0)[b], dev_own(a, 1)[b], dev_own(a, 2)[b], a.ring, a.window, a.n_sink);
+}
 
 // ---- positions in the work list
 
@@ -227,8 +293,9 @@ __device__ __forceinline__ int part_P(const ArgsDev &) { return dev_tab().P; }
 // from c over the range table find the first and the last (entries next to
 // c's, mostly in the same constant-cache line; every range is non-empty).
 template <class A>
-__device__ void seg_info(const A &a, int c, int x, int xhi, Seg &s) {
+__device__ void seg_info(const A &a, int c, int x, int xhi, SegWin &s) {
     const int b = seq_of_x(a, x);
+    if constexpr (A::kWin) s.w = s_win(a, b);
     const int nq = s_nq(a, b), r = s_r(a, b);
     const int items = unit_items(nq, r);
     const int kh = (x - s_ibeg(a, b)) / items;
@@ -254,10 +321,22 @@ __device__ void seg_info(const A &a, int c, int x, int xhi, Seg &s) {
 // ub = flat index of the unit's first item.  Moving forward needs no division.
 struct Cursor {
     int x, u, b, kh, k, ub, items;
+    int gap0, gap, rh0, rh1;   // windowed calls: of sequence b
+    template <class A>
+    __device__ __forceinline__ void seq(const A &a) {
+        if constexpr (A::kWin) {
+            const WinSeq w = s_win(a, b);
+            gap0 = w.gap0;
+            gap = w.gap;
+            rh0 = w.rh0;
+            rh1 = w.rh1;
+        }
+    }
     template <class A>
     __device__ __forceinline__ void set(const A &a, int x_) {
         x = x_;
         b = seq_of_x(a, x);
+        seq(a);
         items = unit_items(s_nq(a, b), s_r(a, b));
         kh = (x - s_ibeg(a, b)) / items;
         u = b * a.Hkv + kh;
@@ -276,6 +355,7 @@ struct Cursor {
                 kh = 0;
                 ++b;
                 items = unit_items(s_nq(a, b), s_r(a, b));
+                seq(a);
             }
         }
     }
@@ -381,7 +461,7 @@ __host__ __device__ __forceinline__ int rvrot(int j) { return ((j >> 1) & 1) + 4
 // tokens into key group n_q/G.  A unit within one CTA is written out directly.
 // Thread tid handles head tid / 128, channel tid % 128.
 template <bool kMass, class A>
-__device__ void finish_unit(const A &a, Smem &sm, const Seg &s, int slot) {
+__device__ void finish_unit(const A &a, Smem &sm, const Seg &s, const WinSeq &w, int slot) {
     const int tid = threadIdx.x, h = tid >> 7, ch = tid & 127;
     const int unit = s.u;
     const int b = s.b, kvh = unit - s.b * a.Hkv;
@@ -443,17 +523,18 @@ __device__ void finish_unit(const A &a, Smem &sm, const Seg &s, int slot) {
         }
     }
     if (kMass && tid == 0) a.stats[unit * 12 + 8] = __int_as_float(s.nq + s.r);
-    if (s.r == a.ring && s.nq + a.G <= a.cap) {
+    // a windowed unit flushes by its sequence's own state
+    const int nq = A::kWin ? w.n_all : s.nq, r = A::kWin ? w.r_all : s.r, rs = A::kWin ? w.rs_all : s.rs;
+    if (r == a.ring && nq + a.G <= a.cap) {
         // flush: the oldest G residual tokens (all in the ring: the new token was
         // appended before its CTA arrived) become key group nq/G and G value tokens
         const uint16_t *kres = a.k_res + (size_t)unit * a.ring * kD;
         const uint16_t *vres = a.v_res + (size_t)unit * a.ring * kD;
-        const int rs = s.rs;
         auto slot_of = [&](int i) { const int t = rs + i; return t >= a.ring ? t - a.ring : t; };
         auto krow = [&](int i, int c) -> const uint16_t * { return kres + (size_t)slot_of(i) * kD + c; };
         auto vrow = [&](int i, int c) -> const uint16_t * { return vres + (size_t)slot_of(i) * kD + c; };
-        const size_t tok0 = (size_t)unit * a.cap + s.nq;
-        const size_t grow = (size_t)unit * a.groups_cap + s.nq / a.G;
+        const size_t tok0 = (size_t)unit * a.cap + nq;
+        const size_t grow = (size_t)unit * a.groups_cap + nq / a.G;
         float *scr = &sm.wy[0][0][0];   // the warp states are summed: free as scratch
         __syncthreads();
         pack_key_group<kThreads>(krow, a.G, a.k_codes_w + tok0 * 8, a.k_scale_w + grow * kD,
@@ -496,9 +577,11 @@ __device__ __forceinline__ void issue_packed(const A &a, uint32_t st, int u, int
 // Residual item i of unit u: logical residual tokens 5i .. 5i+4 (those below r;
 // the rest are zero-filled).  Lanes 0-15 copy chunk `lane` of each K row,
 // lanes 16-31 chunk `lane - 16` of each V row.  Token r-1 is this step's new
-// token, read from k_new / v_new.
+// token, read from k_new / v_new.  A windowed call also zero-fills the hidden
+// tokens [rh0, rh1), so that no value of theirs meets the tensor cores.
 template <class A>
-__device__ __forceinline__ void issue_residual(const A &a, uint32_t st, int u, int i, int r, int rs, int lane) {
+__device__ __forceinline__ void issue_residual(const A &a, uint32_t st, int u, int i, int r, int rs, int lane,
+                                               int rh0, int rh1) {
     const int part = lane >> 4, c = lane & 15;
     const uint16_t *newrow = (part ? a.v_new : a.k_new) + (size_t)u * kD + 8 * c;
     const uint16_t *ring = (part ? a.v_res : a.k_res) + (size_t)u * a.ring * kD + 8 * c;
@@ -508,7 +591,8 @@ __device__ __forceinline__ void issue_residual(const A &a, uint32_t st, int u, i
 #pragma unroll
     for (int j = 0; j < kResTok; ++j) {
         const int ti = t0 + j;
-        const bool ok = ti < r;
+        bool ok = ti < r;
+        if constexpr (A::kWin) ok = ok && (ti < rh0 || ti >= rh1);
         const uint16_t *src = (ti == r - 1 || !ok) ? newrow : ring + (size_t)slot * kD;
         const uint32_t dst = part == 0 ? st + kOffRk + j * 256 + 16 * (c ^ j)
                                        : st + kOffRv + j * 256 + 16 * ((c + rvrot(j)) & 15);
@@ -578,8 +662,13 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
                 issue_q(a, qb0 + pq_slot * 1024, pc.u, lane);
             }
             const int r = s_r(a, pc.b), nri = unit_nri(r);
-            if (pc.k < nri) issue_residual(a, st, pc.u, pc.k, r, s_rs(a, pc.b), lane);
-            else issue_packed(a, st, pc.u, pc.k - nri, lane, pl);
+            if (pc.k < nri) {
+                issue_residual(a, st, pc.u, pc.k, r, s_rs(a, pc.b), lane, pc.rh0, pc.rh1);
+            } else {
+                int j = pc.k - nri;
+                if constexpr (A::kWin) j += j >= pc.gap0 ? pc.gap : 0;
+                issue_packed(a, st, pc.u, j, lane, pl);
+            }
         } else {
             x = xhi;
         }
@@ -642,6 +731,8 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
     int cq_unit = -1, cq_slot = -1, cstage = 0;
     for (;;) {
         const Seg sg = sm.seg;
+        WinSeq win = {};
+        if constexpr (A::kWin) win = sm.seg.w;
         const int u = sg.u, ub = sg.ub, nri = sg.nri, nq = sg.nq, r = sg.r, rs = sg.rs;
 
         float acc[8][4];
@@ -707,7 +798,8 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
                         mma16816(sr, ka, qf[2 * e], qf[2 * e + 1]);
                     }
                 }
-                const bool valid = g_ < n;
+                bool valid = g_ < n;
+                if constexpr (A::kWin) valid = valid && (t0 + g_ < win.rh0 || t0 + g_ >= win.rh1);
                 const float xa = valid ? sr[0] * sl2 : -INFINITY;   // absolute log2 score of token g_, head t_
                 float xv = xa - m_ref;
                 if (__any_sync(0xffffffffu, xv > kLazy)) {
@@ -751,7 +843,20 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
 #undef RSTEP
             } else {
                 // ================= packed item: tokens 32j .. 32j+31 of the unit
-                const int j = k - nri;
+                int j = k - nri;
+                // windowed call: bit i of hid = this lane's token i (2g_, 2g_+1, 16+2g_, 17+2g_) is hidden
+                uint32_t hid = 0;
+                if constexpr (A::kWin) {
+                    j += j >= win.gap0 ? win.gap : 0;
+                    const int p = j * kSlice;
+                    if (p < win.ph1 && p + kSlice > win.ph0) {   // the first or last slice of the hidden run
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int t = p + 2 * g_ + (i & 1) + 8 * (i & 2);
+                            hid |= (uint32_t)(t >= win.ph0 && t < win.ph1) << i;
+                        }
+                    }
+                }
                 if (!vunit) {   // from here on acc holds packed-value units: code 2^(pos-24) per channel pair
                     vunit = true;
 #pragma unroll
@@ -820,13 +925,13 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
                 {
                     const float bias = zcs - m_ref;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) xv[i] = fmaf(sc[i], sl2w, bias);
+                    for (int i = 0; i < 4; ++i) xv[i] = (A::kWin && (hid >> i & 1)) ? -INFINITY : fmaf(sc[i], sl2w, bias);
                 }
                 const float mx = fmaxf(fmaxf(xv[0], xv[1]), fmaxf(xv[2], xv[3]));
                 if (__any_sync(0xffffffffu, mx > kLazy)) {
                     float xa[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) xa[i] = fmaf(sc[i], sl2w, zcs);
+                    for (int i = 0; i < 4; ++i) xa[i] = (A::kWin && (hid >> i & 1)) ? -INFINITY : fmaf(sc[i], sl2w, zcs);
                     const float mn = fmaxf(m_ref, warp_max_g(fmaxf(fmaxf(xa[0], xa[1]), fmaxf(xa[2], xa[3]))));
                     const float al = ex2(m_ref - mn);
                     l *= al;
@@ -854,7 +959,11 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
                 for (int mt = 0; mt < 2; ++mt) {
                     const uint32_t vsw = lds32(S + kOffVs + 2 * (16 * mt + 2 * g_));
                     const uint32_t vzw = lds32(S + kOffVz + 2 * (16 * mt + 2 * g_));
-                    const float2 vsf = unpack_half2(vsw), vzf = unpack_half2(vzw);
+                    float2 vsf = unpack_half2(vsw), vzf = unpack_half2(vzw);
+                    if constexpr (A::kWin) {   // a hidden token's scale or zero may be anything: 0 * inf is not 0
+                        if (hid >> (2 * mt) & 1) vsf.x = vzf.x = 0.f;
+                        if (hid >> (2 * mt) & 2) vsf.y = vzf.y = 0.f;
+                    }
                     const float p0 = ex2(xv[2 * mt]), p1 = ex2(xv[2 * mt + 1]);
                     l += p0 + p1;
                     pz = fmaf(p0, vzf.x, fmaf(p1, vzf.y, pz));
@@ -908,7 +1017,7 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
             for (int q4 = 0; q4 < 4; ++q4) dst[q4] = make_float4(y[4 * q4], y[4 * q4 + 1], y[4 * q4 + 2], y[4 * q4 + 3]);
         }
         if (g_ == 0) sm.wl[warp][t_] = lh * f;
-        finish_unit<kMass>(a, sm, sg, c - sg.first);
+        finish_unit<kMass>(a, sm, sg, win, c - sg.first);
         if (sg.hi >= xhi) break;
         __syncthreads();   // every thread has read sm.seg and the warp states
         if (tid == 0) seg_info(a, c, sg.hi, xhi, sm.seg);
@@ -921,16 +1030,16 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
 // its CTAs take SMs as this grid's CTAs leave them and do their parameter-only
 // set-up there; griddepcontrol.wait holds their first global read until this
 // grid has finished and its writes are visible.
-template <bool kMass>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ ArgsUni a) {
+template <bool kMass, class A>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ A a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     launch_dependents();
     run_cta<kMass, true>(a, *reinterpret_cast<Smem *>(smem_raw), blockIdx.x);
 }
 
 // ragged batch: per-sequence lengths in the parameter table
-template <bool kMass>
-__global__ void __launch_bounds__(kThreads, 1) decode_ragged_kernel(const __grid_constant__ ArgsVar a) {
+template <bool kMass, class A>
+__global__ void __launch_bounds__(kThreads, 1) decode_ragged_kernel(const __grid_constant__ A a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     launch_dependents();
     run_cta<kMass, true>(a, *reinterpret_cast<Smem *>(smem_raw), blockIdx.x);
@@ -962,8 +1071,8 @@ __device__ int dev_first_item(const ArgsDev &a, const long long *wbeg, long long
 // next state of every sequence (append; flush G tokens where the ring is full)
 // once its items are done.  A flush that would pass `cap` is not done: the
 // sequence keeps its state and its status word is set to 1.
-template <bool kMass>
-__global__ void __launch_bounds__(kThreads, 1) decode_dev_kernel(const ArgsDev a) {
+template <bool kMass, class A>
+__global__ void __launch_bounds__(kThreads, 1) decode_dev_kernel(const __grid_constant__ A a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     launch_dependents();
     wait_prior_grid();   // the state table is written by the previous step
@@ -978,6 +1087,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_dev_kernel(const ArgsDev a
         rr[b] = st.y + 1;
         rs[b] = st.z;
         stw[b] = st.w;
+        if constexpr (A::kWin) {
+            dev_own(a, 0)[b] = st.x;
+            dev_own(a, 1)[b] = st.y + 1;
+            dev_own(a, 2)[b] = st.z;
+            const WinSeq w = s_win(a, b);
+            nq[b] = w.nq;
+            rr[b] = w.r;
+            rs[b] = w.rs;
+        }
     }
     __syncthreads();
     // The launch-wide ticket, taken as soon as the state is read (release: this
@@ -1032,6 +1150,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_dev_kernel(const ArgsDev a
     if ((int)blockIdx.x < dev_tab().P) run_cta<kMass, false>(a, *reinterpret_cast<Smem *>(smem_raw), blockIdx.x);
     // the last ticket's CTA: every sequence's new state, by its last warp (the
     // state words kept in shared memory past the CTA's own Smem)
+    if (A::kWin) {   // from here on the sequences' own state
+        nq = dev_own(a, 0);
+        rr = dev_own(a, 1);
+        rs = dev_own(a, 2);
+    }
     if (tid >= kThreads - 32 && __shfl_sync(0xffffffffu, ticket, 31) == gridDim.x - 1)
         for (int b = tid - (kThreads - 32); b < B; b += 32) {
             int4 st = make_int4(nq[b], rr[b], rs[b], stw[b]);   // a set status stays set
@@ -1105,8 +1228,8 @@ std::mutex g_dev_mu;
 bool g_attr_done[kMaxDevices] = {};
 int g_sms[kMaxDevices] = {};
 
-size_t dev_smem_bytes(int B, int P) {
-    return sizeof(Smem) + sizeof(DevTab) + (5 * (size_t)B + 1 + (size_t)P + 1) * sizeof(int);
+size_t dev_smem_bytes(int B, int P) {   // with the windowed calls' own-state arrays
+    return sizeof(Smem) + sizeof(DevTab) + (8 * (size_t)B + 1 + (size_t)P + 1) * sizeof(int);
 }
 
 // the kernels' shared memory is above the 48 KB default: opt in once per device
@@ -1115,16 +1238,19 @@ int ensure_attr(int dev) {
     if (!g_attr_done[dev]) {
         const int smax = (int)dev_smem_bytes(kMaxRaggedSeqs, kMaxCtas);
         const int s = (int)sizeof(Smem);
-        if (cudaFuncSetAttribute(decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, s) != cudaSuccess ||
-            cudaFuncSetAttribute(decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, s) != cudaSuccess ||
-            cudaFuncSetAttribute(decode_ragged_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, s) !=
-                cudaSuccess ||
-            cudaFuncSetAttribute(decode_ragged_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, s) !=
-                cudaSuccess ||
-            cudaFuncSetAttribute(decode_dev_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smax) !=
-                cudaSuccess ||
-            cudaFuncSetAttribute(decode_dev_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smax) !=
-                cudaSuccess)
+        const void *host_planned[] = {
+            (const void *)decode_kernel<false, ArgsUni>,        (const void *)decode_kernel<true, ArgsUni>,
+            (const void *)decode_ragged_kernel<false, ArgsVar>, (const void *)decode_ragged_kernel<true, ArgsVar>,
+            (const void *)decode_kernel<false, ArgsUniWin>,     (const void *)decode_ragged_kernel<false, ArgsVarWin>};
+        const void *device_state[] = {(const void *)decode_dev_kernel<false, ArgsDev>,
+                                      (const void *)decode_dev_kernel<true, ArgsDev>,
+                                      (const void *)decode_dev_kernel<false, ArgsDevWin>};
+        bool ok = true;
+        for (const void *f : host_planned)
+            ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, s) == cudaSuccess;
+        for (const void *f : device_state)
+            ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smax) == cudaSuccess;
+        if (!ok)
             return check_launch("decode_attn: cudaFuncSetAttribute");
         g_attr_done[dev] = true;
     }
@@ -1305,14 +1431,26 @@ int choose_wu(const Shape &s, int sms, bool uniform, int ring) {
     return best_wu;
 }
 
-Plan plan(const minikv_cache *c, int dev) {
+// What a windowed call hides (window = 0: a call without a window).
+struct Window {
+    int window = 0, n_sink = 0;
+};
+// Sequence b's record for the coming step of a host-planned windowed call.
+WinSeq host_win(const minikv_cache *c, int b, const Window &w) {
+    return win_seq(seq_nq(c, b), seq_nres(c, b) + 1, seq_rs(c, b), c->R + c->G, w.window, w.n_sink);
+}
+
+Plan plan(const minikv_cache *c, int dev, const Window &w = Window()) {
     Plan p;
     p.units = c->B * c->Hkv;
     const int ring = c->R + c->G;
     if (c->dseq) {
         // device-state mode: one configuration for every state the cache can hold;
         // the kernel partitions this step's items itself, at boundary weight kWU
-        const long long Wmax = unit_w(c->cap, ring);
+        long long cap = c->cap;
+        if (w.window && cap > (long long)w.window + w.n_sink + 2 * kSlice)   // both ends' slices may be part hidden
+            cap = (long long)w.window + w.n_sink + 2 * kSlice;
+        const long long Wmax = unit_w((int)cap, ring);
         p.P = (int)cta_count((long long)p.units * Wmax, sm_count(dev));
         p.S_max = slots_bound(Wmax, kMinShare);
         if (p.S_max > p.P) p.S_max = p.P;
@@ -1332,6 +1470,11 @@ Plan plan(const minikv_cache *c, int dev) {
         const int q = ragged ? b : 0;
         s.nq[b] = seq_nq(c, q);
         s.r[b] = seq_nres(c, q) + 1;
+        if (w.window) {
+            const WinSeq v = host_win(c, q, w);
+            s.nq[b] = v.nq;
+            s.r[b] = v.r;
+        }
         if (s.nq[b] + s.r[b] > p.max_n) p.max_n = s.nq[b] + s.r[b];
         s.ibeg[b + 1] = s.ibeg[b] + c->Hkv * unit_items(s.nq[b], s.r[b]);
     }
@@ -1447,7 +1590,9 @@ int launch_mass(const Args &a, const Plan &p, float *mass, long long mass_stride
 }  // namespace
 
 int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new, int Hq,
-                  float sm_scale, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream, float *mass) {
+                  float sm_scale, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream, float *mass,
+                  int window, int n_sink) {
+    const Window win = {window, n_sink};
     const int g = Hq / c->Hkv;
     const int ring = c->R + c->G;
     const int nb = c->dseq ? 0 : (c->seq ? c->B : 1);   // device state: checked on the device
@@ -1459,7 +1604,7 @@ int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, con
     if (dev < 0) return fail(MINIKV_ERR_CUDA, "decode_attn: no current CUDA device");
     const int arc = ensure_attr(dev);
     if (arc) return arc;
-    const Plan p = plan(c, dev);
+    const Plan p = plan(c, dev, win);
     const size_t cnt_bytes = decode_counter_bytes(c->B, c->Hkv);
     const size_t part_bytes = (size_t)p.units * p.S_max * 4 * kPartStride * 4;
     size_t need = cnt_bytes + part_bytes;
@@ -1493,34 +1638,64 @@ int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, con
     a.det = g_deterministic.load(std::memory_order_relaxed);
 
     int rc;
+    const size_t smem = c->dseq ? dev_smem_bytes(c->B, p.P) : sizeof(Smem);
     if (c->dseq) {
+        if (window) {
+            ArgsDevWin ad;
+            static_cast<Args &>(ad) = a;
+            ad.window = window;
+            ad.n_sink = n_sink;
+            return launch_pdl(decode_dev_kernel<false, ArgsDevWin>, ad, p.P, smem, stream,
+                              "decode_attn_window (device state)");
+        }
         ArgsDev ad;
         static_cast<Args &>(ad) = a;
-        const size_t smem = dev_smem_bytes(c->B, p.P);
-        rc = mass ? launch_pdl(decode_dev_kernel<true>, ad, p.P, smem, stream, "decode_attn_mass (device state)")
-                  : launch_pdl(decode_dev_kernel<false>, ad, p.P, smem, stream, "decode_attn (device state)");
+        rc = mass ? launch_pdl(decode_dev_kernel<true, ArgsDev>, ad, p.P, smem, stream, "decode_attn_mass (device state)")
+                  : launch_pdl(decode_dev_kernel<false, ArgsDev>, ad, p.P, smem, stream, "decode_attn (device state)");
         if (rc) return rc;
         return mass ? launch_mass(a, p, mass, (long long)c->cap + ring, stream) : MINIKV_OK;
     } else if (c->seq) {
-        ArgsVar av;
-        static_cast<Args &>(av) = a;
-        av.tab.ibeg[0] = 0;
-        for (int b = 0; b < c->B; ++b) {
-            const int nq = seq_nq(c, b), r = seq_nres(c, b) + 1;
+        auto fill = [&](ArgsVar &av) {
+            static_cast<Args &>(av) = a;
+            for (int i = 0; i <= p.P; ++i) av.cta.lo[i] = p.lo[i];
+        };
+        auto seq = [&](ArgsVar &av, int b, int nq, int r, int rs) {
             av.tab.n_q[b] = nq;
             av.tab.r[b] = r;
-            av.tab.res_start[b] = seq_rs(c, b);
+            av.tab.res_start[b] = rs;
+            if (b == 0) av.tab.ibeg[0] = 0;
             av.tab.ibeg[b + 1] = av.tab.ibeg[b] + c->Hkv * unit_items(nq, r);
+        };
+        if (window) {
+            ArgsVarWin av;
+            fill(av);
+            for (int b = 0; b < c->B; ++b) {
+                av.win[b] = host_win(c, b, win);
+                seq(av, b, av.win[b].nq, av.win[b].r, av.win[b].rs);
+            }
+            rc = launch_pdl(decode_ragged_kernel<false, ArgsVarWin>, av, p.P, smem, stream, "decode_attn_window (ragged)");
+        } else {
+            ArgsVar av;
+            fill(av);
+            for (int b = 0; b < c->B; ++b) seq(av, b, seq_nq(c, b), seq_nres(c, b) + 1, seq_rs(c, b));
+            rc = mass ? launch_pdl(decode_ragged_kernel<true, ArgsVar>, av, p.P, smem, stream, "decode_attn_mass (ragged)")
+                      : launch_pdl(decode_ragged_kernel<false, ArgsVar>, av, p.P, smem, stream, "decode_attn (ragged)");
         }
-        for (int i = 0; i <= p.P; ++i) av.cta.lo[i] = p.lo[i];
-        rc = mass ? launch_pdl(decode_ragged_kernel<true>, av, p.P, sizeof(Smem), stream, "decode_attn_mass (ragged)")
-                  : launch_pdl(decode_ragged_kernel<false>, av, p.P, sizeof(Smem), stream, "decode_attn (ragged)");
+    } else if (window) {
+        ArgsUniWin au;
+        static_cast<Args &>(au) = a;
+        for (int i = 0; i <= p.P; ++i) au.cta.lo[i] = p.lo[i];
+        au.win = host_win(c, 0, win);
+        au.n_q = au.win.nq;
+        au.r = au.win.r;
+        au.res_start = au.win.rs;
+        rc = launch_pdl(decode_kernel<false, ArgsUniWin>, au, p.P, smem, stream, "decode_attn_window");
     } else {
         ArgsUni au;
         static_cast<Args &>(au) = a;
         for (int i = 0; i <= p.P; ++i) au.cta.lo[i] = p.lo[i];
-        rc = mass ? launch_pdl(decode_kernel<true>, au, p.P, sizeof(Smem), stream, "decode_attn_mass")
-                  : launch_pdl(decode_kernel<false>, au, p.P, sizeof(Smem), stream, "decode_attn");
+        rc = mass ? launch_pdl(decode_kernel<true, ArgsUni>, au, p.P, smem, stream, "decode_attn_mass")
+                  : launch_pdl(decode_kernel<false, ArgsUni>, au, p.P, smem, stream, "decode_attn");
     }
     if (rc) return rc;
     // host-side state: append, then flush G tokens where the ring is full

@@ -34,7 +34,7 @@ int topk_launch(const float *scores, const uint16_t *k, const uint16_t *v, int B
                 int32_t *idx, uint16_t *k_kept, uint16_t *v_kept, cudaStream_t stream);
 int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new, int Hq,
                   float sm_scale, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream,
-                  float *mass = nullptr);
+                  float *mass = nullptr, int window = 0, int n_sink = 0);
 size_t decode_workspace_bytes(int B, int Hkv, int max_tokens);
 size_t decode_mass_workspace_bytes(int B, int Hq, int Hkv, int max_tokens);
 void decode_set_deterministic(int on);
@@ -336,6 +336,20 @@ int minikv_decode_attn_mass(minikv_cache *c, const uint16_t *q, const uint16_t *
         return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_mass: mass must be 4-byte aligned");
     return decode_launch(c, q, k_new, v_new, Hq, sm_scale, out, ws, ws_bytes, static_cast<cudaStream_t>(stream),
                          mass);
+}
+
+int minikv_decode_attn_window(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new, int Hq,
+                              int window, int n_sink, float sm_scale, uint16_t *out, void *ws, size_t ws_bytes,
+                              void *stream) {
+    int rc = decode_validate(c, q, k_new, v_new, Hq, out);
+    if (rc) return rc;
+    if (window < 1 || n_sink < 0)
+        return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_window: window=%d (at least 1), n_sink=%d (at least 0)", window,
+                    n_sink);
+    if (!ws) return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_window: null workspace");
+    if (!aligned16(ws)) return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_window: workspace must be 16-byte aligned");
+    return decode_launch(c, q, k_new, v_new, Hq, sm_scale, out, ws, ws_bytes, static_cast<cudaStream_t>(stream), nullptr,
+                         window, n_sink);
 }
 
 int minikv_set_deterministic(int on) {

@@ -52,6 +52,7 @@ _SIGS = {
     "minikv_evict_pack": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, ctypes.POINTER(CacheStruct), _P]),
     "minikv_decode_attn": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _P, _I, _F, _P, _P, _Z, _P]),
     "minikv_decode_attn_mass": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _P, _I, _F, _P, _P, _P, _Z, _P]),
+    "minikv_decode_attn_window": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _P, _I, _I, _I, _F, _P, _P, _Z, _P]),
     "minikv_decode_attn_static": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _P, _I, _F, _P, _P]),
     "minikv_set_deterministic": (_I, [_I]),
     "minikv_decode_plan": (_I, [ctypes.POINTER(CacheStruct), ctypes.POINTER(_I), ctypes.POINTER(_I), _P, _I]),
@@ -363,6 +364,25 @@ def decode_attn_mass(cache: MiniKVCache, q: torch.Tensor, k_new: torch.Tensor, v
         ctypes.byref(cache.c), _dev(q, torch.float16, "q"), _dev(k_new, torch.float16, "k_new"),
         _dev(v_new, torch.float16, "v_new"), Hq, float(sm_scale), _dev(out, torch.float16, "out"),
         _dev(mass, torch.float32, "mass"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream, q.device)))
+    return out
+
+
+def decode_attn_window(cache: MiniKVCache, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, window: int,
+                       n_sink: int = 0, sm_scale: float | None = None, out: torch.Tensor | None = None,
+                       ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """decode_attn that attends to the newest `window` tokens (the new one
+    included) and the first `n_sink` of each sequence, in order of arrival."""
+    B, Hq, D = q.shape
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty_like(q)
+    if ws is None:
+        ws = cache.ws
+    _check(lib().minikv_decode_attn_window(
+        ctypes.byref(cache.c), _dev(q, torch.float16, "q"), _dev(k_new, torch.float16, "k_new"),
+        _dev(v_new, torch.float16, "v_new"), Hq, int(window), int(n_sink), float(sm_scale),
+        _dev(out, torch.float16, "out"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream, q.device)))
     return out
 
 

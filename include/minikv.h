@@ -329,6 +329,32 @@ MINIKV_API int minikv_decode_attn_mass(minikv_cache *c, const uint16_t *q, const
                                        float *mass, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * minikv_decode_attn_window -- minikv_decode_attn for a layer with a sliding
+ * window, whose first tokens (sinks) stay visible.
+ * Source: none on the pages; models with a window (the Mistral-7B family of the
+ * LongBench table began with one of 4096) keep the same cache and attend to its
+ * newest tokens only.
+ *   Arguments, cache update and errors as minikv_decode_attn, plus:
+ *   window >= 1, n_sink >= 0.  With the n = n_packed + n_res + 1 tokens of a
+ *       sequence (the new one included) numbered t = 0 .. n-1 in the order they
+ *       entered the cache, the step attends to
+ *         t >= n - window   (the newest `window` tokens, the new one among them)
+ *         t <  n_sink       (the sinks).
+ *       Every other token is left out of the softmax, whatever it holds, and is
+ *       not read (up to the 32-token slices at the two ends of the hidden run).
+ *       window >= n gives minikv_decode_attn's result.
+ *   Nothing is dropped from the cache: a hidden token stays stored, and a flush
+ *   packs the oldest residual tokens as usual.
+ *   Uniform, ragged and device-state caches; ws as for minikv_decode_attn (the
+ *   same bytes and the same reuse; calls of both may share one).
+ * Errors: those of minikv_decode_attn; INVALID_ARG also for window < 1 or
+ * n_sink < 0.
+ */
+MINIKV_API int minikv_decode_attn_window(minikv_cache *c, const uint16_t *q, const uint16_t *k_new,
+                                         const uint16_t *v_new, int Hq, int window, int n_sink, float sm_scale,
+                                         uint16_t *out, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * minikv_decode_attn_static -- minikv_decode_attn without a caller workspace.
  * The paper has no counterpart to this call; it exists for callers that may
  * not allocate device memory: hosts whose device memory is entirely planned by
