@@ -14,11 +14,13 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libminikv.so")
-# The same library with the flash-attention pipeline's bounded waits cut to one
+# The same library with the flash-attention pipelines' bounded waits cut to one
 # poll: its waits give up while their copies are in flight, which exercises the
 # abort path (drain, status word) without any fault.  Only the tests load it.
 WAIT_PROBE_LIB = os.path.join(PKG, "libminikv_waitprobe.so")
-SOURCES = ["minikv_api.cu", "pack.cu", "prefill.cu", "topk.cu", "decode.cu", "decode_static.cu"]
+SOURCES = ["minikv_api.cu", "pack.cu", "prefill.cu", "window_prefill.cu", "topk.cu", "decode.cu", "decode_static.cu"]
+# sources with bounded waits: compiled once more for the wait-probe library
+PROBE_SOURCES = ["prefill.cu", "window_prefill.cu"]
 HEADERS = ["common.cuh", "tc.cuh"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = [
@@ -49,17 +51,19 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
             if ptxas_verbose:
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
-    probe_src = os.path.join(CSRC, "prefill.cu")
-    probe_obj = os.path.join(BUILD, "prefill_waitprobe.o")
-    if force or _stale(probe_obj, [probe_src, *hdrs]):
-        jobs.append([NVCC, *FLAGS, "-DMINIKV_WAIT_LIMIT=1", "-c", probe_src, "-o", probe_obj])
+    probe_objs = list(objs)
+    for src in PROBE_SOURCES:
+        s = os.path.join(CSRC, src)
+        o = os.path.join(BUILD, src.replace(".cu", "_waitprobe.o"))
+        probe_objs[SOURCES.index(src)] = o
+        if force or _stale(o, [s, *hdrs]):
+            jobs.append([NVCC, *FLAGS, "-DMINIKV_WAIT_LIMIT=1", "-c", s, "-o", o])
     with cf.ThreadPoolExecutor(max_workers=min(8, max(1, len(jobs)))) as ex:
         for res in ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs):
             if res.returncode != 0:
                 raise RuntimeError(f"nvcc failed:\n{res.stdout}\n{res.stderr}")
             if ptxas_verbose:
                 print(res.stderr)
-    probe_objs = [probe_obj if o.endswith(os.sep + "prefill.o") else o for o in objs]
     for lib, parts in ((LIB, objs), (WAIT_PROBE_LIB, probe_objs)):
         if force or jobs or _stale(lib, parts):
             tmp = lib + f".tmp{os.getpid()}"

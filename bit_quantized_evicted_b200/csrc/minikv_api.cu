@@ -1,5 +1,6 @@
 // C ABI of libminikv: argument validation, error strings, cache carving, and
 // dispatch to the kernels of pack.cu, prefill.cu, topk.cu and decode.cu.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -38,6 +39,10 @@ int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, con
 size_t decode_workspace_bytes(int B, int Hkv, int max_tokens);
 size_t decode_mass_workspace_bytes(int B, int Hq, int Hkv, int max_tokens);
 void decode_set_deterministic(int on);
+int window_prefill_launch(const uint16_t *q, const uint16_t *k, const uint16_t *v, int B, int Hq, int Hkv, int Tq,
+                          int Tk, int window, int n_sink, float sm_scale, uint16_t *o, void *ws, cudaStream_t stream);
+size_t window_prefill_workspace_bytes(int B, int Hq, int Hkv, int Tq);
+size_t window_prefill_status_words(int B, int Hq, int Hkv, int Tq);
 int decode_plan_info(const minikv_cache *c, int *ctas, int *wu, int *first, int n_first);
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -249,6 +254,67 @@ int minikv_select_prefill_status(const void *ws, size_t ws_bytes, int B, int Hq,
     return MINIKV_OK;
 }
 
+// shape rules of the window prefill, shared with its status call and workspace size
+static int check_window_shape(int B, int Hq, int Hkv, int Tq) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Tq < 1 || Hq % Hkv)
+        return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: B=%d Hq=%d Hkv=%d Tq=%d", B, Hq, Hkv, Tq);
+    if ((size_t)B * Hq > 65535) return fail(MINIKV_ERR_UNSUPPORTED, "window_prefill: B*Hq above 65535");
+    if (window_prefill_status_words(B, Hq, Hkv, Tq) > 0x7fffffff)
+        return fail(MINIKV_ERR_UNSUPPORTED, "window_prefill: more than 2^31 pairs of query tiles");
+    return MINIKV_OK;
+}
+
+int minikv_window_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *v, int B, int Hq, int Hkv, int Tq,
+                          int Tk, int D, int window, int n_sink, float sm_scale, uint16_t *o, void *ws,
+                          size_t ws_bytes, void *stream) {
+    g_err[0] = 0;
+    if (!q || !k || !v || !o || !ws) return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: null pointer");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(ws))
+        return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: pointers must be 16-byte aligned");
+    const int rc = check_window_shape(B, Hq, Hkv, Tq);
+    if (rc) return rc;
+    if (D != kD) return fail(MINIKV_ERR_UNSUPPORTED, "window_prefill: D=%d (only 128)", D);
+    if (Tq > Tk) return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: Tq=%d queries at the end of Tk=%d keys", Tq, Tk);
+    if (Tk > (1 << 30)) return fail(MINIKV_ERR_UNSUPPORTED, "window_prefill: Tk=%d above 2^30", Tk);
+    if (window < 1 || n_sink < 0)
+        return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: window=%d (at least 1), n_sink=%d (at least 0)", window,
+                    n_sink);
+    if (!(sm_scale > 0.f) || !(sm_scale < INFINITY))
+        return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: sm_scale must be positive and finite");
+    const size_t need = window_prefill_workspace_bytes(B, Hq, Hkv, Tq);
+    if (ws_bytes < need)
+        return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: workspace of %zu bytes needed, %zu given", need, ws_bytes);
+    return window_prefill_launch(q, k, v, B, Hq, Hkv, Tq, Tk, window, n_sink, sm_scale, o, ws,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+int minikv_window_prefill_status(const void *ws, size_t ws_bytes, int B, int Hq, int Hkv, int Tq, void *stream,
+                                 unsigned *status) {
+    g_err[0] = 0;
+    if (!ws || !status) return fail(MINIKV_ERR_INVALID_ARG, "window_prefill_status: null pointer");
+    const int rc = check_window_shape(B, Hq, Hkv, Tq);
+    if (rc) return rc;
+    if (ws_bytes < window_prefill_workspace_bytes(B, Hq, Hkv, Tq))
+        return fail(MINIKV_ERR_INVALID_ARG, "window_prefill_status: workspace of %zu bytes is smaller than the call's",
+                    ws_bytes);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned *words = static_cast<const unsigned *>(ws);
+    size_t left = window_prefill_status_words(B, Hq, Hkv, Tq);
+    unsigned got = 0;
+    while (left) {   // the CTAs' words, 1024 at a time
+        unsigned buf[1024];
+        const size_t n = left < 1024 ? left : 1024;
+        cudaError_t e = cudaMemcpyAsync(buf, words, n * sizeof(unsigned), cudaMemcpyDeviceToHost, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        if (e != cudaSuccess) return fail(MINIKV_ERR_CUDA, "window_prefill_status: %s", cudaGetErrorString(e));
+        for (size_t i = 0; i < n; ++i) got |= buf[i];
+        words += n;
+        left -= n;
+    }
+    *status = got;
+    return MINIKV_OK;
+}
+
 int minikv_topk_evict(const float *scores, const uint16_t *k, const uint16_t *v, int B, int Hkv, int T, int D, int W,
                       int keep, int32_t *idx, uint16_t *k_kept, uint16_t *v_kept, void *ws, size_t ws_bytes,
                       void *stream) {
@@ -374,6 +440,9 @@ size_t minikv_workspace_size(int op, int B, int Hq, int Hkv, int T, int D, int W
         case MINIKV_OP_SELECT_PREFILL: return prefill_workspace_bytes(B, Hq, W);
         case MINIKV_OP_TOPK_EVICT: return 0;
         case MINIKV_OP_DECODE_ATTN: return decode_workspace_bytes(B, Hkv, T);
+        case MINIKV_OP_WINDOW_PREFILL:
+            if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || T < 1) return 0;
+            return window_prefill_workspace_bytes(B, Hq, Hkv, T);
         case MINIKV_OP_DECODE_ATTN_MASS:
             if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || T < 0) return 0;
             return decode_mass_workspace_bytes(B, Hq, Hkv, T);

@@ -502,8 +502,10 @@ size_t g_attr_score[kMaxDevices] = {};
 std::mutex g_encode_mu;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
+}  // namespace
+
 // [planes][rows][128] fp16, 128-byte swizzled boxes of 64 x 128 rows
-int make_map(CUtensorMap *m, const void *base, int rows, int planes, const char *what) {
+int make_row_map(CUtensorMap *m, const void *base, int rows, int planes, const char *what) {
     {
         std::lock_guard<std::mutex> lk(g_encode_mu);
         if (!g_encode) {
@@ -511,7 +513,7 @@ int make_map(CUtensorMap *m, const void *base, int rows, int planes, const char 
             void *fn = nullptr;
             if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &qr) != cudaSuccess ||
                 qr != cudaDriverEntryPointSuccess || !fn)
-                return fail(MINIKV_ERR_CUDA, "select_prefill: cuTensorMapEncodeTiled unavailable");
+                return fail(MINIKV_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", what);
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
         }
     }
@@ -521,11 +523,9 @@ int make_map(CUtensorMap *m, const void *base, int rows, int planes, const char 
     const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides, box,
                                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(MINIKV_ERR_CUDA, "select_prefill: tensor map for %s (CUresult %d)", what, (int)r);
+    if (r != CUDA_SUCCESS) return fail(MINIKV_ERR_CUDA, "%s: tensor map (CUresult %d)", what, (int)r);
     return 0;
 }
-
-}  // namespace
 
 // Workspace: the window rows' log-sum-exp [B, Hq, W] fp32, then a 256-byte
 // block whose first word is the call's status (see minikv_select_prefill_status).
@@ -536,8 +536,8 @@ int prefill_launch(const uint16_t *q, const uint16_t *k, const uint16_t *v, int 
                    float sm_scale, uint16_t *o, float *scores, void *ws, cudaStream_t stream) {
     CUtensorMap mq, mk, mv, mo;
     int rc;
-    if ((rc = make_map(&mq, q, T, B * Hq, "q")) || (rc = make_map(&mk, k, T, B * Hkv, "k")) ||
-        (rc = make_map(&mv, v, T, B * Hkv, "v")) || (rc = make_map(&mo, o, T, B * Hq, "o")))
+    if ((rc = make_row_map(&mq, q, T, B * Hq, "select_prefill: q")) || (rc = make_row_map(&mk, k, T, B * Hkv, "select_prefill: k")) ||
+        (rc = make_row_map(&mv, v, T, B * Hkv, "select_prefill: v")) || (rc = make_row_map(&mo, o, T, B * Hq, "select_prefill: o")))
         return rc;
     FaArgs fa;
     fa.lse2 = static_cast<float *>(ws);

@@ -12,6 +12,11 @@
 #include "common.cuh"
 
 namespace minikv {
+
+// Tensor map of [planes][rows][128] fp16 in boxes of 64 x 128 rows, 128-byte
+// swizzled (prefill.cu, host code).  `what` names the call and the tensor in errors.
+int make_row_map(CUtensorMap *m, const void *base, int rows, int planes, const char *what);
+
 namespace tc {
 
 // ---- descriptors ------------------------------------------------------------

@@ -1,0 +1,483 @@
+// minikv_window_prefill: prompt attention with a sliding window and sinks.
+//
+// Query row i of Tq stands at position p = Tk - Tq + i and sees the keys
+// j <= p with p - j < window, and the keys j < n_sink.  Only the 128-key blocks
+// that hold a visible key are read: the sink blocks, then the band.
+//
+// One CTA = two 128-row query tiles of one (sequence, KV head): the KV head's
+// tiles are numbered (position tile, query head of the group), heads fastest,
+// and CTA c takes tiles 2c and 2c + 1, so an even group shares every K / V
+// block between two heads at the same positions.  12 warps:
+//   warp 0      TMA producer: both Q tiles, then K_0, V_0, K_1, V_1, .. into a
+//               ring of 5 x 32 KB;
+//   warp 1      TMEM owner and the single thread issuing tcgen05.mma;
+//   warps 4-7   softmax of tile 0, warps 8-11 of tile 1: thread = query row =
+//               TMEM lane; also the rescale of O and the epilogue.
+// Tensor memory (all 512 columns): S_0, S_1, O_0, O_1 fp32 [128 x 128].  P_t
+// (fp16 pairs, 64 columns) takes the place of S_t once the row is in registers.
+// Issue order: S_0(0), S_1(0), then for every block j and tile t in turn
+// P_t V(j), S_t(j+1): while a tile's softmax works, the tensor cores have the
+// other tile's two products.  A commit covers everything issued before it, so
+// S_t(j+1) complete means O_t holds block j: the softmax may rescale O_t.
+// tcgen05.mma of one thread run in issue order, so S_t(j+1) over P_t(j) is safe.
+//
+// Softmax: base 2, running reference max that moves only when a score passes it
+// by 2^8 (p <= 256 keeps its 11 bits in fp16; O is rescaled rarely).  P is
+// rounded to fp16 for the tensor cores (2^-12 relative a term on average, the
+// precision of the output); the sum is taken in fp32 before that rounding.
+// Hidden keys are -inf before the max, and the reference starts at a finite
+// -1e30, so a block without a visible key for a row leaves that row as it was.
+//
+// A hidden key's value row meets P = 0 in the tensor cores, and 0 * inf is not
+// 0: in the blocks that are only partly visible the softmax threads look at the
+// V tile, and if it holds an infinity or NaN the tile's rows are computed again
+// by slow_row (CUDA cores, visible keys only).
+#include <math.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "tc.cuh"
+
+namespace minikv {
+
+namespace {
+
+constexpr int kM = 128, kN = 128;          // query rows of a tile, keys of a block
+constexpr int kRing = 5;                    // K / V blocks in flight
+constexpr int kThreads = 384;
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 t
+constexpr float kLazy = 8.f;
+constexpr float kNone = -1e30f;             // reference max of a row that has seen nothing
+
+struct Smem {
+    uint16_t q[2][2][kM * 64];       // [tile][64-wide d block], 128-byte swizzle
+    uint16_t kv[kRing][2][kN * 64];
+    uint64_t q_full, full[kRing], empty[kRing];
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int slow[2];                     // tile t met an infinity or NaN in a partly visible V block
+};
+
+struct Args {
+    const uint16_t *q, *k, *v;
+    unsigned *status;   // one word a CTA: 1 = a bounded wait expired, its outputs are not valid
+    int Hq, Hkv, Tq, Tk, window, n_sink;
+    int units, npair, ntile;   // B * Hkv; CTAs and query tiles of a unit
+    float scale_log2;
+};
+
+#ifndef MINIKV_WAIT_LIMIT
+#define MINIKV_WAIT_LIMIT (1u << 26)
+#endif
+
+__device__ __forceinline__ bool wait(Smem &s, uint64_t *bar, uint32_t parity) {
+    if (*reinterpret_cast<volatile int *>(&s.abort)) return false;
+    if (mbar_wait(bar, parity, MINIKV_WAIT_LIMIT)) return true;
+    *reinterpret_cast<volatile int *>(&s.abort) = 1;
+    return false;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// bits [lo, hi) of a 32-bit word, any int lo, hi
+__device__ __forceinline__ uint32_t bits(int lo, int hi) {
+    const uint32_t below_hi = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1;
+    const uint32_t below_lo = lo >= 32 ? 0xffffffffu : lo <= 0 ? 0u : (1u << lo) - 1;
+    return below_hi & ~below_lo;
+}
+
+// One query tile: query head, first query row, and the rows' first and last position.
+struct Tile {
+    int h, q0, p0, p1;
+};
+__device__ __forceinline__ Tile tile_of(const Args &a, int kvh, int i) {
+    const int g = a.Hq / a.Hkv, pt = i / g;
+    Tile t;
+    t.h = kvh * g + i - pt * g;
+    t.q0 = pt * kM;
+    t.p0 = a.Tk - a.Tq + t.q0;
+    t.p1 = min(t.p0 + kM - 1, a.Tk - 1);
+    return t;
+}
+// The CTA's key blocks: n_s sink blocks, then band blocks lo .. hi.
+struct Blocks {
+    int n_s, lo, n;
+    __device__ __forceinline__ int at(int j) const { return j < n_s ? j : lo + j - n_s; }
+};
+__device__ __forceinline__ Blocks blocks_of(const Args &a, int p0, int p1) {
+    Blocks b;
+    b.lo = max(0, p0 - (a.window - 1)) / kN;
+    b.n_s = min(b.lo, (int)(((long long)a.n_sink + kN - 1) / kN));
+    b.n = b.n_s + p1 / kN - b.lo + 1;
+    return b;
+}
+
+// Row `row` of query head plane bh from scratch, visible keys only (fp32, one thread a row).
+__device__ __noinline__ void slow_row(const Args &a, size_t qrow, size_t kvplane, int p, uint16_t *dst, uint32_t sw) {
+    float o[kD];
+#pragma unroll
+    for (int d = 0; d < kD; ++d) o[d] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    const uint4 *q = reinterpret_cast<const uint4 *>(a.q + qrow * kD);
+    const int lo = max(0, p - (a.window - 1));
+    for (int j = 0; j <= p; ++j) {
+        if (j < lo && j >= a.n_sink) j = lo;
+        const uint4 *kr = reinterpret_cast<const uint4 *>(a.k + (kvplane * a.Tk + j) * kD);
+        const uint4 *vr = reinterpret_cast<const uint4 *>(a.v + (kvplane * a.Tk + j) * kD);
+        float x = 0.f;
+        for (int c = 0; c < 16; ++c) {
+            float qa[8], ka[8];
+            h8_to_f(__ldg(q + c), qa);
+            h8_to_f(__ldg(kr + c), ka);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x = fmaf(qa[i], ka[i], x);
+        }
+        x *= a.scale_log2;
+        const float mn = fmaxf(m, x);
+        const float al = m == mn ? 1.f : exp2f(m - mn), w = x == -INFINITY ? 0.f : exp2f(x - mn);
+        m = mn;
+        l = fmaf(l, al, w);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            float va[8];
+            h8_to_f(__ldg(vr + c), va);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[8 * c + i] = fmaf(o[8 * c + i], al, w * va[i]);
+        }
+    }
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {   // as the epilogue writes it: 16-byte chunk c of the row
+        uint4 w;
+        w.x = pack_half2(o[8 * c] * inv, o[8 * c + 1] * inv);
+        w.y = pack_half2(o[8 * c + 2] * inv, o[8 * c + 3] * inv);
+        w.z = pack_half2(o[8 * c + 4] * inv, o[8 * c + 5] * inv);
+        w.w = pack_half2(o[8 * c + 6] * inv, o[8 * c + 7] * inv);
+        *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(dst) + (c >> 3) * (kM * 128) +
+                                   (((c & 7) ^ sw) << 4)) = w;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    window_fa_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
+                     const __grid_constant__ Args a) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    Smem &s = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // the pairs with the longest bands first, all units side by side: their K / V bands overlap in L2
+    const int pair = a.npair - 1 - (int)blockIdx.x / a.units, unit = (int)blockIdx.x % a.units;
+    const int b = unit / a.Hkv, kvh = unit - b * a.Hkv;
+    const Tile t0 = tile_of(a, kvh, 2 * pair);
+    const bool two = 2 * pair + 1 < a.ntile;
+    const Tile t1 = two ? tile_of(a, kvh, 2 * pair + 1) : t0;   // an odd last tile is computed twice, stored once
+    const Blocks blk = blocks_of(a, min(t0.p0, t1.p0), max(t0.p1, t1.p1));
+
+    if (tid == 0) {
+        mbar_init(&s.q_full, 1);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&s.s_full[t], 1);
+            mbar_init(&s.p_full[t], 128);
+            mbar_init(&s.o_done[t], 1);
+            s.slow[t] = 0;
+        }
+        mbar_init(&s.drain, 1);
+        s.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tc::tmem_alloc(&s.tmem_base, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s.tmem_base;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+        if (warp == 0 && lane == 0) {
+            // ---------------- producer
+            tc::prefetch_map(&map_q);
+            tc::prefetch_map(&map_k);
+            tc::prefetch_map(&map_v);
+            mbar_arrive_expect_tx(&s.q_full, 4 * kM * 128);
+            for (int t = 0; t < 2; ++t) {
+                const Tile &ti = t ? t1 : t0;
+                tc::tma_load_3d(s.q[t][0], &map_q, 0, ti.q0, b * a.Hq + ti.h, &s.q_full);
+                tc::tma_load_3d(s.q[t][1], &map_q, 64, ti.q0, b * a.Hq + ti.h, &s.q_full);
+            }
+            int issued = 0;
+            for (int e = 0; e < 2 * blk.n; ++e) {
+                const int st = e % kRing;
+                if (e >= kRing && !wait(s, &s.empty[st], (e / kRing - 1) & 1)) break;
+                const CUtensorMap *m = e & 1 ? &map_v : &map_k;
+                const int row = blk.at(e >> 1) * kN;
+                mbar_arrive_expect_tx(&s.full[st], 2 * kN * 128);
+                tc::tma_load_3d(s.kv[st][0], m, 0, row, unit, &s.full[st]);
+                tc::tma_load_3d(s.kv[st][1], m, 64, row, unit, &s.full[st]);
+                issued = e + 1;
+            }
+            if (*reinterpret_cast<volatile int *>(&s.abort)) {   // let the loads queued here land before the CTA exits
+                mbar_wait(&s.q_full, 0);
+                for (int e = issued > kRing ? issued - kRing : 0; e < issued; ++e)
+                    mbar_wait(&s.full[e % kRing], (e / kRing) & 1);
+            }
+        } else if (warp == 1 && lane == 0) {
+            // ---------------- MMA issuer
+            constexpr uint32_t id_s = tc::idesc_f16(kM, kN, false, false);
+            constexpr uint32_t id_pv = tc::idesc_f16(kM, kD, false, true);
+            auto full = [&](int e) { return wait(s, &s.full[e % kRing], (e / kRing) & 1); };
+            auto issue_s = [&](int t, int j) {
+                const int st = (2 * j) % kRing;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc::mma_ss(tmem + kColS + t * kN, tc::sdesc_sw128(smem_addr(s.q[t][kk >> 2]) + (kk & 3) * 32, 16, 1024),
+                               tc::sdesc_sw128(smem_addr(s.kv[st][kk >> 2]) + (kk & 3) * 32, 16, 1024), id_s, kk > 0);
+                tc::commit(&s.s_full[t]);
+            };
+            auto issue_pv = [&](int t, int j) {
+                const int st = (2 * j + 1) % kRing;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc::mma_ts(tmem + kColO + t * kD, tmem + kColS + t * kN + kk * 8,
+                               tc::sdesc_sw128(smem_addr(s.kv[st][0]) + kk * 2048, 2 * kN * 64, 1024), id_pv,
+                               (j > 0) || (kk > 0));
+            };
+            bool ok = wait(s, &s.q_full, 0) && full(0);
+            if (ok) {
+                tc::fence_after_sync();
+                issue_s(0, 0);
+                issue_s(1, 0);
+                tc::commit(&s.empty[0]);
+            }
+            for (int j = 0; ok && j < blk.n; ++j) {
+                const bool next = j + 1 < blk.n;
+                ok = full(2 * j + 1) && (!next || full(2 * j + 2));
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    ok = ok && wait(s, &s.p_full[t], j & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    issue_pv(t, j);
+                    if (next) issue_s(t, j + 1);
+                    else tc::commit(&s.o_done[t]);
+                }
+                if (!ok) break;
+                tc::commit(&s.empty[(2 * j + 1) % kRing]);
+                if (next) tc::commit(&s.empty[(2 * j + 2) % kRing]);
+            }
+            // every MMA issued here has finished with shared and tensor memory before the CTA frees them
+            tc::commit(&s.drain);
+            mbar_wait(&s.drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- softmax warps
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
+        const int t = warp >= 8;
+        const Tile ti = t ? t1 : t0;
+        const int r = 32 * (warp & 3) + lane;
+        const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lane_off + kColS + t * kN, to = tmem + lane_off + kColO + t * kD;
+        const int p = ti.p0 + r;   // this row's position
+        const float sc = a.scale_log2;
+        float m_ref = kNone;
+        unsigned long long l2a = 0ull, l2b = 0ull;
+        bool ok = true;
+        for (int j = 0; j < blk.n; ++j) {
+            const int k0 = blk.at(j) * kN;
+            // every row sees the whole block: no key after the first row's, all in the last row's window or sinks
+            const bool whole = k0 + kN - 1 <= ti.p0 && (k0 >= ti.p1 - (a.window - 1) || k0 + kN <= a.n_sink);
+            ok = __all_sync(0xffffffffu, wait(s, &s.s_full[t], j & 1));
+            if (!ok) break;
+            tc::fence_after_sync();
+            uint32_t x[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                tc::tmem_ld32(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
+            tc::wait_ld();
+            if (!whole) {
+                const int hi = p + 1 - k0, lo = p - (a.window - 1) - k0, sk = min(a.n_sink - k0, hi);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t seen = bits(lo - 32 * c, hi - 32 * c) | bits(0, sk - 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!(seen >> i & 1)) x[32 * c + i] = __float_as_uint(-INFINITY);
+                }
+                // key row r of the V block: an infinity or NaN in it?
+                const int e = 2 * j + 1;
+                ok = __all_sync(0xffffffffu, wait(s, &s.full[e % kRing], (e / kRing) & 1));
+                if (!ok) break;
+                uint32_t bad = 0;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(&s.kv[e % kRing][c >> 3][r * 64 + 8 * ((c ^ r) & 7)]);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {   // exponent 31 carries into bit 15 of each half
+                        bad |= (u[i] & 0x7C007C00u) + 0x04000400u;
+                    }
+                }
+                if (bad & 0x80008000u) *reinterpret_cast<volatile int *>(&s.slow[t]) = 1;
+            }
+            float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 128; c += 8) {
+                mx0 = max3(mx0, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                mx1 = max3(mx1, __uint_as_float(x[c + 2]), __uint_as_float(x[c + 3]));
+                mx2 = max3(mx2, __uint_as_float(x[c + 4]), __uint_as_float(x[c + 5]));
+                mx3 = max3(mx3, __uint_as_float(x[c + 6]), __uint_as_float(x[c + 7]));
+            }
+            const float mxs = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sc;
+            float alpha = 1.f;
+            const bool grow = mxs > m_ref + kLazy;
+            if (grow) {
+                alpha = ex2(m_ref - mxs);
+                m_ref = mxs;
+                const unsigned long long al2 = f2pack(alpha, alpha);
+                l2a = fmul2(l2a, al2);
+                l2b = fmul2(l2b, al2);
+            }
+            const unsigned long long sc2 = f2pack(sc, sc), nm2 = f2pack(-m_ref, -m_ref);
+            uint32_t ph[64];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+                float e0, e1;
+                f2unpack(ffma2(f2pack(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sc2, nm2), e0, e1);
+                const float p0 = ex2(e0), p1 = ex2(e1);
+                ph[c] = pack_half2(p0, p1);
+                if (c & 1) l2b = fadd2(l2b, f2pack(p0, p1));
+                else l2a = fadd2(l2a, f2pack(p0, p1));
+            }
+            tc::tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(&ph[0]));
+            tc::tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&ph[32]));
+            if (j > 0 && __any_sync(0xffffffffu, grow)) {   // O holds every block before j (see above)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(to + 32 * c, o);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                    tc::tmem_st32(to + 32 * c, o);
+                }
+            }
+            tc::wait_st();
+            tc::fence_before_sync();
+            tc::mbar_arrive(&s.p_full[t]);
+        }
+        // ---------------- epilogue: O / l -> fp16 -> swizzled smem (the Q tile) -> TMA store
+        if (ok) ok = __all_sync(0xffffffffu, wait(s, &s.o_done[t], 0));
+        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + t) : "memory");   // slow[t] is complete
+        if (ok) {
+            tc::fence_after_sync();
+            unsigned char *qbytes = reinterpret_cast<unsigned char *>(s.q[t]);
+            if (*reinterpret_cast<volatile int *>(&s.slow[t])) {
+                if (ti.q0 + r < a.Tq)
+                    slow_row(a, ((size_t)b * a.Hq + ti.h) * a.Tq + ti.q0 + r, unit, p,
+                             reinterpret_cast<uint16_t *>(qbytes + r * 128), r & 7);
+            } else {
+                float la, lb;
+                f2unpack(fadd2(l2a, l2b), la, lb);
+                const float inv = 1.f / (la + lb);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(to + 32 * c, o);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {   // 16-byte chunk: d = 32c + 8u .. +7
+                        const int d = 32 * c + 8 * u;
+                        const int kb = d >> 6, ch = (d & 63) >> 3;
+                        uint4 w;
+                        w.x = pack_half2(__uint_as_float(o[8 * u + 0]) * inv, __uint_as_float(o[8 * u + 1]) * inv);
+                        w.y = pack_half2(__uint_as_float(o[8 * u + 2]) * inv, __uint_as_float(o[8 * u + 3]) * inv);
+                        w.z = pack_half2(__uint_as_float(o[8 * u + 4]) * inv, __uint_as_float(o[8 * u + 5]) * inv);
+                        w.w = pack_half2(__uint_as_float(o[8 * u + 6]) * inv, __uint_as_float(o[8 * u + 7]) * inv);
+                        *reinterpret_cast<uint4 *>(qbytes + kb * (kM * 128) + r * 128 + ((ch ^ (r & 7)) << 4)) = w;
+                    }
+                }
+            }
+            tc::fence_proxy_async_smem();
+        }
+        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + t) : "memory");
+        if (ok && (warp & 3) == 0 && lane == 0 && (t == 0 || two)) {
+            tc::tma_store_3d(&map_o, s.q[t][0], 0, ti.q0, b * a.Hq + ti.h);
+            tc::tma_store_3d(&map_o, s.q[t][1], 64, ti.q0, b * a.Hq + ti.h);
+            tc::bulk_commit_group();
+            tc::bulk_wait_all();
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_dealloc(tmem, 512);
+    if (tid == 0) a.status[blockIdx.x] = s.abort ? 1u : 0u;
+}
+
+std::mutex g_attr_mu;
+bool g_attr[kMaxDevices] = {};
+
+long long grid_of(int B, int Hq, int Hkv, int Tq) {
+    const long long tiles = ((long long)Tq + kM - 1) / kM * (Hq / Hkv);
+    return (long long)B * Hkv * ((tiles + 1) / 2);
+}
+
+}  // namespace
+
+// Workspace: a status word a CTA.
+size_t window_prefill_status_words(int B, int Hq, int Hkv, int Tq) { return (size_t)grid_of(B, Hq, Hkv, Tq); }
+size_t window_prefill_workspace_bytes(int B, int Hq, int Hkv, int Tq) {
+    return (window_prefill_status_words(B, Hq, Hkv, Tq) * 4 + 255) / 256 * 256;
+}
+
+int window_prefill_launch(const uint16_t *q, const uint16_t *k, const uint16_t *v, int B, int Hq, int Hkv, int Tq,
+                          int Tk, int window, int n_sink, float sm_scale, uint16_t *o, void *ws, cudaStream_t stream) {
+    CUtensorMap mq, mk, mv, mo;
+    int rc;
+    if ((rc = make_row_map(&mq, q, Tq, B * Hq, "window_prefill: q")) ||
+        (rc = make_row_map(&mk, k, Tk, B * Hkv, "window_prefill: k")) ||
+        (rc = make_row_map(&mv, v, Tk, B * Hkv, "window_prefill: v")) ||
+        (rc = make_row_map(&mo, o, Tq, B * Hq, "window_prefill: o")))
+        return rc;
+    Args a;
+    a.q = q; a.k = k; a.v = v;
+    a.status = static_cast<unsigned *>(ws);
+    a.Hq = Hq; a.Hkv = Hkv; a.Tq = Tq; a.Tk = Tk;
+    a.window = window < Tk ? window : Tk;   // the same keys, and no overflow in the kernel's differences
+    a.n_sink = n_sink < Tk ? n_sink : Tk;
+    a.units = B * Hkv;
+    a.ntile = (Tq + kM - 1) / kM * (Hq / Hkv);
+    a.npair = (a.ntile + 1) / 2;
+    a.scale_log2 = sm_scale * kLog2e;
+    const size_t smem = sizeof(Smem) + 1024;
+    const int dev = current_device();
+    if (dev < 0) return fail(MINIKV_ERR_CUDA, "window_prefill: no current CUDA device");
+    {
+        std::lock_guard<std::mutex> lk(g_attr_mu);
+        if (!g_attr[dev]) {
+            if (cudaFuncSetAttribute(window_fa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+                cudaSuccess)
+                return check_launch("window_prefill: attribute");
+            g_attr[dev] = true;
+        }
+    }
+    window_fa_kernel<<<(unsigned)grid_of(B, Hq, Hkv, Tq), kThreads, smem, stream>>>(mq, mk, mv, mo, a);
+    return check_launch("window_prefill");
+}
+
+}  // namespace minikv

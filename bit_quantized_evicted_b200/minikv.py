@@ -20,7 +20,7 @@ LIB_PATH = os.environ.get("MINIKV_LIB", os.path.join(_PKG, "libminikv.so"))
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "minikv.h")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CAPACITY, ERR_CUDA = 0, -1, -2, -3, -4
-OP_SELECT_PREFILL, OP_TOPK_EVICT, OP_DECODE_ATTN, OP_DECODE_ATTN_MASS = 1, 2, 3, 4
+OP_SELECT_PREFILL, OP_TOPK_EVICT, OP_DECODE_ATTN, OP_DECODE_ATTN_MASS, OP_WINDOW_PREFILL = 1, 2, 3, 4, 5
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -48,6 +48,8 @@ _SIGS = {
     "minikv_evict_pack_seq": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, ctypes.POINTER(CacheStruct), _I, _P]),
     "minikv_select_prefill": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _Z, _P]),
     "minikv_select_prefill_status": (_I, [_P, _Z, _I, _I, _I, _P, ctypes.POINTER(ctypes.c_uint)]),
+    "minikv_window_prefill": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _Z, _P]),
+    "minikv_window_prefill_status": (_I, [_P, _Z, _I, _I, _I, _I, _P, ctypes.POINTER(ctypes.c_uint)]),
     "minikv_topk_evict": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
     "minikv_evict_pack": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, ctypes.POINTER(CacheStruct), _P]),
     "minikv_decode_attn": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _P, _I, _F, _P, _P, _Z, _P]),
@@ -288,6 +290,40 @@ def select_prefill_status(ws: torch.Tensor, B: int, Hq: int, W: int, stream=None
     L = library or lib()
     _check(L.minikv_select_prefill_status(_dev(ws, torch.uint8, "ws"), ws.numel(), B, Hq, W,
                                           _stream(stream, ws.device), ctypes.byref(st)))
+    return int(st.value)
+
+
+def window_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, n_sink: int = 0,
+                   sm_scale: float | None = None, o: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                   stream=None, library=None) -> torch.Tensor:
+    """Attention output o [B, Hq, Tq, D] of the last Tq of Tk positions: a query
+    sees the newest `window` keys up to its own and the first `n_sink`."""
+    B, Hq, Tq, D = q.shape
+    Hkv, Tk = k.shape[1], k.shape[2]
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not match")
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    if o is None:
+        o = torch.empty_like(q)
+    elif o.shape != q.shape:
+        raise ValueError(f"o {tuple(o.shape)} does not match q {tuple(q.shape)}")
+    if ws is None:
+        ws = torch.empty(max(workspace_size(OP_WINDOW_PREFILL, B, Hq, Hkv, Tq, D), 256), dtype=torch.uint8,
+                         device=q.device)
+    _check((library or lib()).minikv_window_prefill(
+        _dev(q, torch.float16, "q"), _dev(k, torch.float16, "k"), _dev(v, torch.float16, "v"), B, Hq, Hkv, Tq, Tk, D,
+        int(window), int(n_sink), float(sm_scale), _dev(o, torch.float16, "o"), _dev(ws, torch.uint8, "ws"), ws.numel(),
+        _stream(stream, q.device)))
+    return o
+
+
+def window_prefill_status(ws: torch.Tensor, B: int, Hq: int, Hkv: int, Tq: int, stream=None, library=None) -> int:
+    """Status of the last window_prefill on `ws` (synchronizes the stream): 0 =
+    finished, bit 0 = a bounded wait expired."""
+    st = ctypes.c_uint(0)
+    _check((library or lib()).minikv_window_prefill_status(_dev(ws, torch.uint8, "ws"), ws.numel(), B, Hq, Hkv, Tq,
+                                                           _stream(stream, ws.device), ctypes.byref(st)))
     return int(st.value)
 
 

@@ -217,6 +217,43 @@ MINIKV_API int minikv_select_prefill_status(const void *ws, size_t ws_bytes, int
                                             unsigned *status);
 
 /*
+ * minikv_window_prefill -- prompt attention for a layer with a sliding window,
+ * whose first tokens (sinks) stay visible.
+ * Source: none on the pages (see minikv_decode_attn_window, its decode step).
+ *   q [B, Hq, Tq, D], k, v [B, Hkv, Tk, D] fp16, 1 <= Tq <= Tk: the queries are
+ *   the last Tq of Tk positions (Tq = Tk: a whole prompt; Tq < Tk: a chunk
+ *   against everything before it).
+ *   o [B, Hq, Tq, D] fp16: with p = Tk - Tq + i the position of query row i,
+ *       o_i = sum_j softmax_j(sm_scale * q_i.k_j) v_j over the keys j <= p with
+ *       p - j < window or j < n_sink.
+ *   window >= 1, n_sink >= 0; window >= Tk is causal attention over all keys.
+ *   A key outside a row's set takes no part in that row, whatever it holds (an
+ *   infinity or NaN among the hidden values costs time, never a result).
+ *   Key blocks no row sees are not read.
+ *   sm_scale > 0 (the usual 1/sqrt(D)).
+ *   ws: device scratch of minikv_workspace_size(MINIKV_OP_WINDOW_PREFILL, B, Hq,
+ *       Hkv, Tq, D, 0) bytes, no initial contents required; it holds the call's
+ *       status words (minikv_window_prefill_status).
+ * Errors: INVALID_ARG (null, misaligned, Tq > Tk, Hq % Hkv, window < 1,
+ * n_sink < 0, sm_scale <= 0, ws too small), UNSUPPORTED (D != 128, B*Hq above
+ * 65535, Tk above 2^30), CUDA (tensor-map encoding or launch failed).
+ */
+MINIKV_API int minikv_window_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *v, int B, int Hq, int Hkv,
+                                     int Tq, int Tk, int D, int window, int n_sink, float sm_scale, uint16_t *o,
+                                     void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * minikv_window_prefill_status -- did the last minikv_window_prefill on this
+ * workspace finish its work?  As minikv_select_prefill_status: *status = 0, or
+ * bit 0 set if a bounded wait expired in some CTA (o is then not valid).
+ *   ws, ws_bytes, B, Hq, Hkv, Tq: as passed to that call.
+ * Queues device-to-host copies of 4 bytes a CTA on `stream` and synchronizes it.
+ * Errors: INVALID_ARG (null, shape, ws smaller than the call's), CUDA.
+ */
+MINIKV_API int minikv_window_prefill_status(const void *ws, size_t ws_bytes, int B, int Hq, int Hkv, int Tq,
+                                            void *stream, unsigned *status);
+
+/*
  * minikv_topk_evict -- adaptive KV: keep the tokens that matter.
  * Source: summary page, glossary 术语表 "adaptive KV" (keep KV states by
  * importance); notesum LongBench table, "MiniKV Pyramid" (the caller picks
@@ -382,6 +419,7 @@ MINIKV_API int minikv_decode_attn_static(minikv_cache *c, const uint16_t *q, con
 #define MINIKV_OP_TOPK_EVICT     2
 #define MINIKV_OP_DECODE_ATTN    3
 #define MINIKV_OP_DECODE_ATTN_MASS 4
+#define MINIKV_OP_WINDOW_PREFILL 5   /* T = Tq */
 
 /*
  * minikv_decode_plan -- how the next minikv_decode_attn (or _mass, _static)
