@@ -18,10 +18,11 @@ LIB = os.path.join(PKG, "libminikv.so")
 # poll: its waits give up while their copies are in flight, which exercises the
 # abort path (drain, status word) without any fault.  Only the tests load it.
 WAIT_PROBE_LIB = os.path.join(PKG, "libminikv_waitprobe.so")
-SOURCES = ["minikv_api.cu", "pack.cu", "prefill.cu", "window_prefill.cu", "topk.cu", "decode.cu", "decode_static.cu"]
+SOURCES = ["minikv_api.cu", "pack.cu", "prefill.cu", "window_prefill.cu", "topk.cu", "decode.cu",
+           "decode_static.cu", "prefix.cu"]
 # sources with bounded waits: compiled once more for the wait-probe library
-PROBE_SOURCES = ["prefill.cu", "window_prefill.cu"]
-HEADERS = ["common.cuh", "tc.cuh"]
+PROBE_SOURCES = ["prefill.cu", "window_prefill.cu", "prefix.cu"]
+HEADERS = ["common.cuh", "tc.cuh", "prefix.cuh"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -54,6 +54,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "prefix.cuh"
 
 namespace minikv {
 
@@ -279,6 +280,19 @@ struct ArgsVarWin : ArgsVar {
 struct ArgsDevWin : ArgsDev {
     static constexpr bool kWin = true;
     int window, n_sink;
+};
+// ---- a batch behind a shared prefix: each mode's arguments with the prefix pass's partials
+struct ArgsUniPre : ArgsUni {
+    static constexpr bool kPre = true;
+    PreTab pre;
+};
+struct ArgsVarPre : ArgsVar {
+    static constexpr bool kPre = true;
+    PreTab pre;
+};
+struct ArgsDevPre : ArgsDev {
+    static constexpr bool kPre = true;
+    PreTab pre;
 };
 __device__ __forceinline__ WinSeq s_win(const ArgsUniWin &a, int) { return a.win; }
 __device__ __forceinline__ WinSeq s_win(const ArgsVarWin &a, int b) { return a.win[b]; }
@@ -514,6 +528,35 @@ __device__ void finish_unit(const A &a, Smem &sm, const Seg &s, const WinSeq &w,
                     M = Mn;
                 }
             }
+    }
+    if constexpr (A::kPre) {
+        // the row's states over the shared prefix, from the pass before this kernel
+        const PreTab &t = a.pre;
+        const int place = t.listed ? t.place[b] : b;
+        if (place >= 0 && h < a.g) {
+            const int row = place * a.g + h, pu = (row >> t.lgN) * a.Hkv + kvh, n = row & ((1 << t.lgN) - 1);
+            const int c0 = pre_cta(t, pu * t.tpu), c1 = pre_cta(t, pu * t.tpu + t.tpu - 1);
+            for (int s0 = c0; s0 <= c1; s0 += 8) {
+                float ms[8], ls[8], ys[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool ok = s0 + j <= c1;
+                    const float *p = t.part + (((size_t)(s0 + j + pu) << t.lgN) + n) * kPreStride;
+                    ms[j] = ok ? __ldcg(p + 128) : -INFINITY;
+                    ls[j] = ok ? __ldcg(p + 129) : 0.f;
+                    ys[j] = ok ? __ldcg(p + ch) : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float m = ms[j], Mn = fmaxf(M, m);
+                    const float fo = (M == -INFINITY) ? 0.f : ex2(M - Mn);
+                    const float fs = (m == -INFINITY) ? 0.f : ex2(m - Mn);
+                    L = fmaf(L, fo, ls[j] * fs);
+                    Y = fmaf(Y, fo, ys[j] * fs);
+                    M = Mn;
+                }
+            }
+        }
     }
     if (h < a.g) {
         a.out[((size_t)b * Hq + kvh * a.g + h) * kD + ch] = f2h(__fdividef(Y, L));
@@ -1241,10 +1284,12 @@ int ensure_attr(int dev) {
         const void *host_planned[] = {
             (const void *)decode_kernel<false, ArgsUni>,        (const void *)decode_kernel<true, ArgsUni>,
             (const void *)decode_ragged_kernel<false, ArgsVar>, (const void *)decode_ragged_kernel<true, ArgsVar>,
-            (const void *)decode_kernel<false, ArgsUniWin>,     (const void *)decode_ragged_kernel<false, ArgsVarWin>};
+            (const void *)decode_kernel<false, ArgsUniWin>,     (const void *)decode_ragged_kernel<false, ArgsVarWin>,
+            (const void *)decode_kernel<false, ArgsUniPre>,     (const void *)decode_ragged_kernel<false, ArgsVarPre>};
         const void *device_state[] = {(const void *)decode_dev_kernel<false, ArgsDev>,
                                       (const void *)decode_dev_kernel<true, ArgsDev>,
-                                      (const void *)decode_dev_kernel<false, ArgsDevWin>};
+                                      (const void *)decode_dev_kernel<false, ArgsDevWin>,
+                                      (const void *)decode_dev_kernel<false, ArgsDevPre>};
         bool ok = true;
         for (const void *f : host_planned)
             ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, s) == cudaSuccess;
@@ -1591,7 +1636,7 @@ int launch_mass(const Args &a, const Plan &p, float *mass, long long mass_stride
 
 int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new, int Hq,
                   float sm_scale, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream, float *mass,
-                  int window, int n_sink) {
+                  int window, int n_sink, const PreTab *pre) {
     const Window win = {window, n_sink};
     const int g = Hq / c->Hkv;
     const int ring = c->R + c->G;
@@ -1648,6 +1693,13 @@ int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, con
             return launch_pdl(decode_dev_kernel<false, ArgsDevWin>, ad, p.P, smem, stream,
                               "decode_attn_window (device state)");
         }
+        if (pre) {
+            ArgsDevPre ad;
+            static_cast<Args &>(ad) = a;
+            ad.pre = *pre;
+            return launch_pdl(decode_dev_kernel<false, ArgsDevPre>, ad, p.P, smem, stream,
+                              "decode_attn_prefix (device state)");
+        }
         ArgsDev ad;
         static_cast<Args &>(ad) = a;
         rc = mass ? launch_pdl(decode_dev_kernel<true, ArgsDev>, ad, p.P, smem, stream, "decode_attn_mass (device state)")
@@ -1674,6 +1726,12 @@ int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, con
                 seq(av, b, av.win[b].nq, av.win[b].r, av.win[b].rs);
             }
             rc = launch_pdl(decode_ragged_kernel<false, ArgsVarWin>, av, p.P, smem, stream, "decode_attn_window (ragged)");
+        } else if (pre) {
+            ArgsVarPre av;
+            fill(av);
+            for (int b = 0; b < c->B; ++b) seq(av, b, seq_nq(c, b), seq_nres(c, b) + 1, seq_rs(c, b));
+            av.pre = *pre;
+            rc = launch_pdl(decode_ragged_kernel<false, ArgsVarPre>, av, p.P, smem, stream, "decode_attn_prefix (ragged)");
         } else {
             ArgsVar av;
             fill(av);
@@ -1690,6 +1748,12 @@ int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, con
         au.r = au.win.r;
         au.res_start = au.win.rs;
         rc = launch_pdl(decode_kernel<false, ArgsUniWin>, au, p.P, smem, stream, "decode_attn_window");
+    } else if (pre) {
+        ArgsUniPre au;
+        static_cast<Args &>(au) = a;
+        for (int i = 0; i <= p.P; ++i) au.cta.lo[i] = p.lo[i];
+        au.pre = *pre;
+        rc = launch_pdl(decode_kernel<false, ArgsUniPre>, au, p.P, smem, stream, "decode_attn_prefix");
     } else {
         ArgsUni au;
         static_cast<Args &>(au) = a;

@@ -5,6 +5,7 @@
 #include <stdio.h>
 
 #include "common.cuh"
+#include "prefix.cuh"
 
 namespace minikv {
 
@@ -35,7 +36,8 @@ int topk_launch(const float *scores, const uint16_t *k, const uint16_t *v, int B
                 int32_t *idx, uint16_t *k_kept, uint16_t *v_kept, cudaStream_t stream);
 int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new, int Hq,
                   float sm_scale, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream,
-                  float *mass = nullptr, int window = 0, int n_sink = 0);
+                  float *mass = nullptr, int window = 0, int n_sink = 0,
+                  const PreTab *pre = nullptr);
 size_t decode_workspace_bytes(int B, int Hkv, int max_tokens);
 size_t decode_mass_workspace_bytes(int B, int Hq, int Hkv, int max_tokens);
 void decode_set_deterministic(int on);
@@ -43,6 +45,11 @@ int window_prefill_launch(const uint16_t *q, const uint16_t *k, const uint16_t *
                           int Tk, int window, int n_sink, float sm_scale, uint16_t *o, void *ws, cudaStream_t stream);
 size_t window_prefill_workspace_bytes(int B, int Hq, int Hkv, int Tq);
 size_t window_prefill_status_words(int B, int Hq, int Hkv, int Tq);
+int prefix_launch(const minikv_cache *p, const int *shared, int B, const uint16_t *q, int Hq, float sm_scale, void *ws,
+                  cudaStream_t stream, PreTab *tab);
+size_t prefix_workspace_bytes(int B, int Hq, int Hkv);
+size_t prefix_status_words();
+size_t decode_call_workspace_bytes(const minikv_cache *c);
 int decode_plan_info(const minikv_cache *c, int *ctas, int *wu, int *first, int n_first);
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -254,6 +261,24 @@ int minikv_select_prefill_status(const void *ws, size_t ws_bytes, int B, int Hq,
     return MINIKV_OK;
 }
 
+// OR of `left` status words on the device, read 1024 at a time (synchronizes the stream)
+static int read_status(const void *ws, size_t left, cudaStream_t s, const char *what, unsigned *status) {
+    const unsigned *words = static_cast<const unsigned *>(ws);
+    unsigned got = 0;
+    while (left) {
+        unsigned buf[1024];
+        const size_t n = left < 1024 ? left : 1024;
+        cudaError_t e = cudaMemcpyAsync(buf, words, n * sizeof(unsigned), cudaMemcpyDeviceToHost, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        if (e != cudaSuccess) return fail(MINIKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+        for (size_t i = 0; i < n; ++i) got |= buf[i];
+        words += n;
+        left -= n;
+    }
+    *status = got;
+    return MINIKV_OK;
+}
+
 // shape rules of the window prefill, shared with its status call and workspace size
 static int check_window_shape(int B, int Hq, int Hkv, int Tq) {
     if (B < 1 || Hq < 1 || Hkv < 1 || Tq < 1 || Hq % Hkv)
@@ -297,22 +322,8 @@ int minikv_window_prefill_status(const void *ws, size_t ws_bytes, int B, int Hq,
     if (ws_bytes < window_prefill_workspace_bytes(B, Hq, Hkv, Tq))
         return fail(MINIKV_ERR_INVALID_ARG, "window_prefill_status: workspace of %zu bytes is smaller than the call's",
                     ws_bytes);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned *words = static_cast<const unsigned *>(ws);
-    size_t left = window_prefill_status_words(B, Hq, Hkv, Tq);
-    unsigned got = 0;
-    while (left) {   // the CTAs' words, 1024 at a time
-        unsigned buf[1024];
-        const size_t n = left < 1024 ? left : 1024;
-        cudaError_t e = cudaMemcpyAsync(buf, words, n * sizeof(unsigned), cudaMemcpyDeviceToHost, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-        if (e != cudaSuccess) return fail(MINIKV_ERR_CUDA, "window_prefill_status: %s", cudaGetErrorString(e));
-        for (size_t i = 0; i < n; ++i) got |= buf[i];
-        words += n;
-        left -= n;
-    }
-    *status = got;
-    return MINIKV_OK;
+    return read_status(ws, window_prefill_status_words(B, Hq, Hkv, Tq), static_cast<cudaStream_t>(stream),
+                       "window_prefill_status", status);
 }
 
 int minikv_topk_evict(const float *scores, const uint16_t *k, const uint16_t *v, int B, int Hkv, int T, int D, int W,
@@ -418,6 +429,57 @@ int minikv_decode_attn_window(minikv_cache *c, const uint16_t *q, const uint16_t
                          window, n_sink);
 }
 
+int minikv_decode_attn_prefix(minikv_cache *c, const minikv_cache *prefix, const int *shared, const uint16_t *q,
+                              const uint16_t *k_new, const uint16_t *v_new, int Hq, float sm_scale, uint16_t *out,
+                              void *ws, size_t ws_bytes, void *stream) {
+    int rc = decode_validate(c, q, k_new, v_new, Hq, out);
+    if (rc) return rc;
+    rc = check_cache(prefix);
+    if (rc) return rc;
+    if (prefix->B != 1 || prefix->Hkv != c->Hkv)
+        return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: prefix cache with B=%d Hkv=%d (B=1 and the batch's Hkv=%d)",
+                    prefix->B, prefix->Hkv, c->Hkv);
+    if (prefix->dseq)
+        return fail(MINIKV_ERR_UNSUPPORTED, "decode_attn_prefix: the prefix cache's state must be on the host");
+    if (prefix->Gv != prefix->D)
+        return fail(MINIKV_ERR_UNSUPPORTED, "decode_attn_prefix: prefix value group Gv=%d (needs Gv = D)", prefix->Gv);
+    if (prefix->k_codes == c->k_codes || prefix->k_res == c->k_res)
+        return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: the prefix and the batch share cache memory");
+    if (shared && c->B > MINIKV_MAX_RAGGED_SEQS)
+        return fail(MINIKV_ERR_UNSUPPORTED, "decode_attn_prefix: flags for B=%d sequences (at most %d)", c->B,
+                    MINIKV_MAX_RAGGED_SEQS);
+    if (!(sm_scale > 0.f) || !(sm_scale < INFINITY))
+        return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: sm_scale must be positive and finite");
+    if (!ws) return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: null workspace");
+    if (!aligned16(ws)) return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: workspace must be 16-byte aligned");
+    const size_t own = up256(decode_call_workspace_bytes(c)), pre = prefix_workspace_bytes(c->B, Hq, c->Hkv);
+    if (ws_bytes < own + pre)
+        return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: workspace of %zu bytes needed, %zu given", own + pre,
+                    ws_bytes);
+    // the prefix pass's part lies at the end, where no call on this workspace keeps arrival counters
+    char *pws = static_cast<char *>(ws) + (ws_bytes - pre) / 256 * 256;
+    PreTab tab;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    rc = prefix_launch(prefix, shared, c->B, q, Hq, sm_scale, pws, s, &tab);
+    if (rc) return rc;
+    return decode_launch(c, q, k_new, v_new, Hq, sm_scale, out, ws, (size_t)(pws - static_cast<char *>(ws)), s, nullptr, 0,
+                         0, tab.P ? &tab : nullptr);
+}
+
+int minikv_decode_attn_prefix_status(const void *ws, size_t ws_bytes, int B, int Hq, int Hkv, void *stream,
+                                     unsigned *status) {
+    g_err[0] = 0;
+    if (!ws || !status) return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix_status: null pointer");
+    if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv)
+        return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix_status: B=%d Hq=%d Hkv=%d", B, Hq, Hkv);
+    const size_t pre = prefix_workspace_bytes(B, Hq, Hkv);
+    if (ws_bytes < pre)
+        return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix_status: workspace of %zu bytes is smaller than the call's",
+                    ws_bytes);
+    return read_status(static_cast<const char *>(ws) + (ws_bytes - pre) / 256 * 256, prefix_status_words(),
+                       static_cast<cudaStream_t>(stream), "decode_attn_prefix_status", status);
+}
+
 int minikv_set_deterministic(int on) {
     decode_set_deterministic(on);
     return MINIKV_OK;
@@ -440,6 +502,9 @@ size_t minikv_workspace_size(int op, int B, int Hq, int Hkv, int T, int D, int W
         case MINIKV_OP_SELECT_PREFILL: return prefill_workspace_bytes(B, Hq, W);
         case MINIKV_OP_TOPK_EVICT: return 0;
         case MINIKV_OP_DECODE_ATTN: return decode_workspace_bytes(B, Hkv, T);
+        case MINIKV_OP_DECODE_ATTN_PREFIX:
+            if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || T < 0) return 0;
+            return up256(decode_workspace_bytes(B, Hkv, T)) + up256(prefix_workspace_bytes(B, Hq, Hkv)) + 256;
         case MINIKV_OP_WINDOW_PREFILL:
             if (B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || T < 1) return 0;
             return window_prefill_workspace_bytes(B, Hq, Hkv, T);

@@ -21,6 +21,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "minikv.h")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CAPACITY, ERR_CUDA = 0, -1, -2, -3, -4
 OP_SELECT_PREFILL, OP_TOPK_EVICT, OP_DECODE_ATTN, OP_DECODE_ATTN_MASS, OP_WINDOW_PREFILL = 1, 2, 3, 4, 5
+OP_DECODE_ATTN_PREFIX = 6
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -55,6 +56,9 @@ _SIGS = {
     "minikv_decode_attn": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _P, _I, _F, _P, _P, _Z, _P]),
     "minikv_decode_attn_mass": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _P, _I, _F, _P, _P, _P, _Z, _P]),
     "minikv_decode_attn_window": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _P, _I, _I, _I, _F, _P, _P, _Z, _P]),
+    "minikv_decode_attn_prefix": (_I, [ctypes.POINTER(CacheStruct), ctypes.POINTER(CacheStruct), _P, _P, _P, _P, _I, _F,
+                                       _P, _P, _Z, _P]),
+    "minikv_decode_attn_prefix_status": (_I, [_P, _Z, _I, _I, _I, _P, ctypes.POINTER(ctypes.c_uint)]),
     "minikv_decode_attn_static": (_I, [ctypes.POINTER(CacheStruct), _P, _P, _P, _I, _F, _P, _P]),
     "minikv_set_deterministic": (_I, [_I]),
     "minikv_decode_plan": (_I, [ctypes.POINTER(CacheStruct), ctypes.POINTER(_I), ctypes.POINTER(_I), _P, _I]),
@@ -420,6 +424,49 @@ def decode_attn_window(cache: MiniKVCache, q: torch.Tensor, k_new: torch.Tensor,
         _dev(v_new, torch.float16, "v_new"), Hq, int(window), int(n_sink), float(sm_scale),
         _dev(out, torch.float16, "out"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream, q.device)))
     return out
+
+
+def shared_rows(flags):
+    """Host flags (one a sequence) in the form decode_attn_prefix takes without converting."""
+    return (_I * len(flags))(*(1 if f else 0 for f in flags))
+
+
+def decode_attn_prefix(cache: MiniKVCache, prefix: MiniKVCache, q: torch.Tensor, k_new: torch.Tensor,
+                       v_new: torch.Tensor, shared=None, sm_scale: float | None = None,
+                       out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None,
+                       library=None) -> torch.Tensor:
+    """decode_attn of a batch whose sequences (all, or those flagged in `shared`)
+    also attend to every token of `prefix`, a cache of one sequence.  The default
+    workspace is made once per cache, zero-filled, and kept on it."""
+    B, Hq, D = q.shape
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty_like(q)
+    if shared is not None:
+        if len(shared) != B:
+            raise ValueError(f"{len(shared)} flags for {B} sequences")
+        if not isinstance(shared, ctypes.Array):
+            shared = shared_rows(shared)
+    if ws is None:
+        need = workspace_size(OP_DECODE_ATTN_PREFIX, B, Hq, cache.Hkv, cache.cap + cache.R + cache.G, D)
+        if getattr(cache, "ws_prefix", None) is None or cache.ws_prefix.numel() < need:
+            cache.ws_prefix = torch.zeros(need, dtype=torch.uint8, device=cache.device)
+        ws = cache.ws_prefix
+    _check((library or lib()).minikv_decode_attn_prefix(
+        ctypes.byref(cache.c), ctypes.byref(prefix.c), shared, _dev(q, torch.float16, "q"),
+        _dev(k_new, torch.float16, "k_new"), _dev(v_new, torch.float16, "v_new"), Hq, float(sm_scale),
+        _dev(out, torch.float16, "out"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream, q.device)))
+    return out
+
+
+def decode_attn_prefix_status(ws: torch.Tensor, B: int, Hq: int, Hkv: int, stream=None, library=None) -> int:
+    """Status of the last decode_attn_prefix on `ws` (synchronizes the stream): 0
+    = finished, bit 0 = a bounded wait of the prefix pass expired."""
+    st = ctypes.c_uint(0)
+    _check((library or lib()).minikv_decode_attn_prefix_status(_dev(ws, torch.uint8, "ws"), ws.numel(), B, Hq, Hkv,
+                                                               _stream(stream, ws.device), ctypes.byref(st)))
+    return int(st.value)
 
 
 def decode_plan(cache) -> tuple:

@@ -392,6 +392,50 @@ MINIKV_API int minikv_decode_attn_window(minikv_cache *c, const uint16_t *q, con
                                          uint16_t *out, void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * minikv_decode_attn_prefix -- minikv_decode_attn for a batch whose sequences
+ * share a prefix (a system prompt, a document): the prefix is packed once, in a
+ * cache of its own, and read once a step for the whole batch.
+ * Source: none on the pages; serving answers many requests on one text, and the
+ * packed prefix is the compact layout of 方法论.
+ *   Arguments, cache update and errors as minikv_decode_attn, plus:
+ *   prefix: a cache of B = 1 with c's Hkv, loaded by minikv_quant_pack or
+ *       minikv_evict_pack (its G, R and cap may differ from c's), state on the
+ *       host.  It is only read, and may be empty.
+ *   shared: HOST array [B], nonzero for the sequences that attend to the
+ *       prefix; NULL: all of them.  Read during the call.
+ *   out_h = sum_t softmax_t(sm_scale * q_h . kappa_t) nu_t over every token of
+ *   the prefix (if the sequence shares it) and of the sequence's own cache, the
+ *   new token included.  The new token and a flush go to c.
+ *   sm_scale > 0.
+ *   ws: minikv_workspace_size(MINIKV_OP_DECODE_ATTN_PREFIX, B, Hq, Hkv,
+ *       cap + R + G, D, 0) bytes with c's cap, R and G, zero-filled before its
+ *       first use, reusable like the workspace of minikv_decode_attn.
+ * Two kernels are queued: the prefix pass, whose partial softmax states depend
+ * on neither the sequences' lengths nor on chance, and the decode kernel, which
+ * merges them.  In a captured step the prefix's length and `shared` are those
+ * of the capture.
+ * Errors: those of minikv_decode_attn; INVALID_ARG also for a prefix cache of
+ * another shape or the batch's own, sm_scale <= 0; UNSUPPORTED for a prefix
+ * cache with device-resident state or Gv != D, and for `shared` with B above
+ * MINIKV_MAX_RAGGED_SEQS.
+ */
+MINIKV_API int minikv_decode_attn_prefix(minikv_cache *c, const minikv_cache *prefix, const int *shared,
+                                         const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new, int Hq,
+                                         float sm_scale, uint16_t *out, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * minikv_decode_attn_prefix_status -- did the prefix pass of the last
+ * minikv_decode_attn_prefix on this workspace finish its work?  As
+ * minikv_select_prefill_status: *status = 0, or bit 0 set if a bounded wait
+ * expired in some CTA (that call's `out` is then not valid).
+ *   ws, ws_bytes, B, Hq, Hkv: as passed to that call.
+ * Queues a device-to-host copy on `stream` and synchronizes it.
+ * Errors: INVALID_ARG (null, shape, ws smaller than the call's), CUDA.
+ */
+MINIKV_API int minikv_decode_attn_prefix_status(const void *ws, size_t ws_bytes, int B, int Hq, int Hkv, void *stream,
+                                                unsigned *status);
+
+/*
  * minikv_decode_attn_static -- minikv_decode_attn without a caller workspace.
  * The paper has no counterpart to this call; it exists for callers that may
  * not allocate device memory: hosts whose device memory is entirely planned by
@@ -420,6 +464,7 @@ MINIKV_API int minikv_decode_attn_static(minikv_cache *c, const uint16_t *q, con
 #define MINIKV_OP_DECODE_ATTN    3
 #define MINIKV_OP_DECODE_ATTN_MASS 4
 #define MINIKV_OP_WINDOW_PREFILL 5   /* T = Tq */
+#define MINIKV_OP_DECODE_ATTN_PREFIX 6
 
 /*
  * minikv_decode_plan -- how the next minikv_decode_attn (or _mass, _static)
