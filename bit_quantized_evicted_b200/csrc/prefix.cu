@@ -5,29 +5,42 @@
 //
 // Both products are turned over, so that a tile of 128 tokens fills the M = 128
 // of a tcgen05.mma and the N query rows (16, 32, 64 or 128) are its N:
-//   S^T [128 tokens x N] = K^ [tokens x channels] Q^T,
-//   O^T [128 channels x N] += V^^T [channels x tokens] P^T.
+//   S'^T [128 tokens x N] = K' [tokens x channels] Q^T,
+//   O'^T [128 channels x N] += V'^T [channels x tokens] P^T.
 // With the rows as M a batch of 16 rows would pay for 128.
 //
-//   K^  fp16, the A operand in tensor memory: the thread of a token dequantizes
-//       its 128 channels (rounded to fp16, the type the key was stored in before
-//       it was quantized) and stores them to its own lane.
-//   V^  fp16 in shared memory, [token][channel], read as an M-major A operand.
+// Exact operands.  A dequantized c s + z needs more than fp16's 11 bits, but
+// (c - o) s / 2 with o = 1 or 2 is a whole multiple of s / 2 between -2 and 2: an
+// fp16 number, never above the largest.  With c s + z = (c - o) s + (z + o s):
+//   score = 2 K' q + T,  T = q (z + s), one number a (key group, row), o = 1;
+//   out   = 2 V' p + sum_t p_t (z + o s)_t, one number a row; o = 1 for even, 2
+//           for odd tokens, so that both sums stay near the output's size (the
+//           tensor cores' long sums lose bits of the larger).
+// Both corrections, and the sum of p, are small products on mma.sync with fp32
+// sums: T = Q [z | s] of the tile's four 32-token quarters (each within one key
+// group), and [1; hi(z + o s); lo(z + o s)] P.  Only P is rounded (to fp16, half
+// a step of the output's own type).
+//
+//   K'  fp16, the A operand in tensor memory: the thread of a token dequantizes
+//       its 128 channels and stores them to its own lane.
+//   V'  fp16 in shared memory, [token][channel], read as an M-major A operand.
 //   Q   [row][channel], P^T [token][row] in shared memory, the B operands.
 // A code word's pairs (i, i + 8) come out of one mask each, so channels are
 // kept in that order: position 16 w + 2 i + b is channel 16 w + i + 8 b.  Q is
-// laid out alike, and the epilogue puts O^T's lanes back.
+// laid out alike, and the epilogue puts O'^T's lanes back.
 //
 // Dequantization: c | 0x6400 is the fp16 number 1024 + c (code bits at mantissa
-// bit 2I: 1024 + 4^I c), one fma makes it c exactly, a second c * scale + zero
-// with one rounding.
+// bit 2I: 1024 + 4^I c); one fma makes it (c - o) / 2, one product (c - o) s / 2.
 //
-// 20 warps: 1 issues the MMAs, 4-7 dequantize K, 8-11 V (a thread a token),
-// 12-19 softmax (thread = token lane, half of the N columns each).  S, K^, V^
-// and P have two buffers.  The reference max of a row moves only when a score
-// passes it by 2^8; then the eight warps' column maxima meet in shared memory
-// and O^T is rescaled.  Sums stay in registers, one a token lane and row, until
-// the segment ends.
+// The loops are kept short on purpose: with the five roles unrolled over their
+// tiles, 7.7 of 14 warps waited for instructions (N = 64; 3.3 us a tile).
+//
+// 24 warps: 0 and 2 compute T (half of the rows each), 1 issues the MMAs, 4-7
+// dequantize K, 8-11 V (a thread a token), 12-19 softmax (thread = token lane,
+// half of the rows each), 20-23 the sums over P (a quarter of the rows each).  S, K', V' and P have two
+// buffers.  The reference max of a row moves only when a score passes it by 2^8;
+// then the column maxima of a half's four warps meet in shared memory and O'^T
+// and the sums are rescaled.
 #include <math.h>
 
 #include <mutex>
@@ -41,9 +54,8 @@ namespace minikv {
 namespace {
 
 constexpr int kTile = 128;      // tokens of a tile
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 constexpr float kLazy = 8.f;
-constexpr float kNone = -1e30f;
 
 template <int N>
 struct Smem {
@@ -51,10 +63,14 @@ struct Smem {
     uint16_t v[2][2][kTile * 64];       // [stage][64-channel block][token][64], 128-byte swizzle
     uint16_t p[2][kNB][kTile * 64];     // [stage][64-row block][token][64]
     uint16_t q[2][N * 64];              // [64-channel block][row][64]
-    uint32_t ksz[4][2][128];            // per K warp: scale pairs [64], zero pairs [64] of its group, two tiles
-    float m[N], alpha[N];
-    float wmax[4][N], wsum[4][N];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], drain;
+    uint32_t ksz[2][4][128];            // [stage][quarter]: scale pairs [64], zero pairs [64] of its key group
+    uint32_t vz[2][2][kTile / 2];       // [stage][hi, lo]: fp16 z + o s of the value tokens
+    float tz[2][4][N];                  // [stage][quarter][row]: T in log2 units
+    float bias[8][N / 2];               // a softmax warp's T - reference of the tile in hand
+    float m[N], alpha[2][N], l[N], pz[N];
+    float wmax[4][N];
+    int resc[2][2];                     // [stage][half]: the tile moved the references (alpha holds the factors)
+    uint64_t k_full[2], k_empty[2], kz_full[2], t_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain;
     uint32_t tmem_base;
     int abort;
 };
@@ -72,53 +88,102 @@ struct Args {
     short seq[MINIKV_MAX_RAGGED_SEQS];   // listed: sequence of each place
 };
 
+// Polls before a wait gives up; each may suspend the thread for kSuspendNs (4 s in all).
 #ifndef MINIKV_WAIT_LIMIT
-#define MINIKV_WAIT_LIMIT (1u << 26)
+#define MINIKV_WAIT_LIMIT (1u << 18)
 #endif
+constexpr uint32_t kSuspendNs = 16384;
 
+// Bounded waits of the CTA: once one gives up, every wait that is not already
+// over returns false, so all roles reach the segment's end.  The common case, a
+// phase that is over, takes a handful of instructions: twenty warps in five
+// roles share the instruction caches.
+// up to n polls
+__device__ __forceinline__ uint32_t poll(uint64_t *bar, uint32_t parity, uint32_t n) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b32 n;\n mov.b32 n, %4;\n"
+        "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n @p bra OVER;\n"
+        " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra POLL;\n"
+        "OVER:\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done) : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendNs), "r"(n) : "memory");
+    return done;
+}
+constexpr uint32_t kPolls = MINIKV_WAIT_LIMIT < 256 ? MINIKV_WAIT_LIMIT : 256;   // between two looks at the abort flag
 template <class S>
-__device__ __forceinline__ bool wait(S &s, uint64_t *bar, uint32_t parity) {
-    if (*reinterpret_cast<volatile int *>(&s.abort)) return false;
-    if (mbar_wait(bar, parity, MINIKV_WAIT_LIMIT)) return true;
-    *reinterpret_cast<volatile int *>(&s.abort) = 1;
-    return false;
+__device__ __forceinline__ bool wait(S &s, uint64_t *bar, uint32_t parity) {   // one thread
+    for (uint32_t i = 0; !poll(bar, parity, kPolls); i += kPolls) {
+        if (i + kPolls >= MINIKV_WAIT_LIMIT) *reinterpret_cast<volatile int *>(&s.abort) = 1;
+        if (*reinterpret_cast<volatile int *>(&s.abort)) return false;
+    }
+    return true;
 }
 template <class S>
-__device__ __forceinline__ bool wait_warp(S &s, uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait(s, bar, parity));
+__device__ __forceinline__ bool wait_warp(S &s, uint64_t *bar, uint32_t parity) {   // a warp's 32 lanes
+    for (uint32_t i = 0; !__all_sync(0xffffffffu, poll(bar, parity, kPolls)); i += kPolls) {
+        if (i + kPolls >= MINIKV_WAIT_LIMIT) *reinterpret_cast<volatile int *>(&s.abort) = 1;
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&s.abort))) return false;
+    }
+    return true;
+}
+// The warp's arrival, once all its lanes are here.
+__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-// fp16x2 (x, x) bits of 4^-I and -1024 * 4^-I
-__host__ __device__ constexpr uint32_t pow_m(int I) { return 0x00010001u * (uint32_t)((15 - 2 * I) << 10); }
-__host__ __device__ constexpr uint32_t neg_1024(int I) { return 0x00010001u * (0x8000u | (uint32_t)((25 - 2 * I) << 10)); }
-// codes (i, i + 8) of a word as fp16x2; x = word, y = word >> 10
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+constexpr uint32_t kHalf2 = 0x38003800u;   // fp16x2 (0.5, 0.5)
+// fp16x2 bits of 4^-I / 2 and of -(1024 4^-I + o) / 2, o = 1 (512.5, 128.5, 32.5, 8.5, 2.5) or 2 (513, 129, 33, 9, 3)
+__host__ __device__ constexpr uint32_t code_mul(int I) { return 0x00010001u * (uint32_t)((14 - 2 * I) << 10); }
+__host__ __device__ constexpr uint32_t code_add(int I, int o) {
+    return 0x00010001u * (0x8000u | (uint32_t)((24 - 2 * I) << 10) | ((uint32_t)o << (2 * I)));
+}
+// The offset of a lane's token, as the five addends above.
+struct Offset {
+    uint32_t add[5];
+    __device__ __forceinline__ explicit Offset(bool two) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) add[i] = two ? code_add(i, 2) : code_add(i, 1);
+    }
+};
+// (c - o) / 2 of codes (i, i + 8) of a word as fp16x2; x = word, y = word >> 10
 template <int I>
-__device__ __forceinline__ uint32_t code2(uint32_t x, uint32_t y) {
+__device__ __forceinline__ uint32_t code2(uint32_t x, uint32_t y, const Offset &o) {
     constexpr int J = I < 5 ? I : I - 5;
     const uint32_t t = ((I < 5 ? x : y) & (0x00030003u << (2 * J))) | 0x64006400u;
-    return hfma2(t, pow_m(J), neg_1024(J));
+    return hfma2(t, code_mul(J), o.add[J]);
 }
-// word `x` of 16 codes -> 8 fp16 pairs c * s + z; s and z as functions of the pair
-template <class FS, class FZ>
-__device__ __forceinline__ void dequant_word(uint32_t x, FS s, FZ z, uint32_t *out) {
+// word `x` of 16 codes -> 8 fp16 pairs (c - o) s / 2; s as a function of the pair
+template <class FS>
+__device__ __forceinline__ void dequant_word(uint32_t x, const Offset &o, FS s, uint32_t *out) {
     const uint32_t y = x >> 10;
-    out[0] = hfma2(code2<0>(x, y), s(0), z(0));
-    out[1] = hfma2(code2<1>(x, y), s(1), z(1));
-    out[2] = hfma2(code2<2>(x, y), s(2), z(2));
-    out[3] = hfma2(code2<3>(x, y), s(3), z(3));
-    out[4] = hfma2(code2<4>(x, y), s(4), z(4));
-    out[5] = hfma2(code2<5>(x, y), s(5), z(5));
-    out[6] = hfma2(code2<6>(x, y), s(6), z(6));
-    out[7] = hfma2(code2<7>(x, y), s(7), z(7));
+    out[0] = hmul2(code2<0>(x, y, o), s(0));
+    out[1] = hmul2(code2<1>(x, y, o), s(1));
+    out[2] = hmul2(code2<2>(x, y, o), s(2));
+    out[3] = hmul2(code2<3>(x, y, o), s(3));
+    out[4] = hmul2(code2<4>(x, y, o), s(4));
+    out[5] = hmul2(code2<5>(x, y, o), s(5));
+    out[6] = hmul2(code2<6>(x, y, o), s(6));
+    out[7] = hmul2(code2<7>(x, y, o), s(7));
 }
 // 16 fp16 channels (two 16-byte chunks) into pair order
 __device__ __forceinline__ void pair_order(const uint4 &lo, const uint4 &hi, uint32_t *out) {
@@ -169,32 +234,36 @@ __device__ __forceinline__ void load_rows(Smem<N> &s, const Args &a, const Seg &
         *reinterpret_cast<uint4 *>(dst + ((ch ^ (n & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
         *reinterpret_cast<uint4 *>(dst + (((ch + 1) ^ (n & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
     }
-    if (tid < N) s.m[tid] = kNone;
+    if (tid < N) s.m[tid] = 0.f;   // the first tile sets it to its maximum
     tc::fence_proxy_async_smem();
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ Args a) {
-    constexpr int C = N / 2;                 // columns of a softmax thread
-    constexpr int CH = C < 16 ? C : 16;      // columns in registers at a time
+    constexpr int C = N / 2;                 // rows of a softmax thread
+    constexpr int CH = C < 32 ? C : 32;      // columns a tensor-memory load
+    constexpr int kTW = N == 16 ? 1 : 2;     // T warps
+    constexpr int kSW = N == 16 ? 2 : 4;     // sum warps
     constexpr uint32_t kColS = 0, kColO = 2 * N, kColK = 3 * N;
     constexpr uint32_t kCols = 3 * N + 128 <= 256 ? 256 : 512;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     using S = Smem<N>;
     S &s = *reinterpret_cast<S *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3;
+    const int g_ = lane >> 2, t_ = lane & 3;
     const int c = blockIdx.x;
 
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.k_full[i], 128);
-            mbar_init(&s.k_empty[i], 1);
-            mbar_init(&s.v_full[i], 128);
-            mbar_init(&s.v_empty[i], 1);
+            mbar_init(&s.k_full[i], 4);     // warps
+            mbar_init(&s.k_empty[i], 1 + kTW);   // S has read K', the T warps the scales and zeros
+            mbar_init(&s.kz_full[i], 4);
+            mbar_init(&s.t_full[i], kTW);
+            mbar_init(&s.v_full[i], 4);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_full[i], 256);
-            mbar_init(&s.o_done[i], 1);
+            mbar_init(&s.p_full[i], 8);
+            mbar_init(&s.o_done[i], 1 + kSW);    // O'^T has the tile; the sum warps have its sums
         }
         mbar_init(&s.drain, 1);
         s.abort = 0;
@@ -210,6 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 
     const int lo = (int)((long long)c * a.tab.T / a.tab.P), hi = (int)((long long)(c + 1) * a.tab.T / a.tab.P);
     int it = 0;   // tiles of the CTA before this segment: the barriers' phases run on
+    // phase parity of tile k's use of a two-stage barrier, and of the use before it
+    auto ph = [](int k) { return (uint32_t)(k >> 1) & 1; };
+    auto ph_prev = [](int k) { return (uint32_t)((k >> 1) - 1) & 1; };
 
     // Every role runs the segments in step: the query rows, a block barrier, the
     // role's own work on the segment's tiles, a block barrier.  (Each role has its
@@ -227,56 +299,109 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             sync_all();
             work(sg);
             it += sg.n;
-            sync_all();   // the segment's barriers, Q, references and O^T are free
+            sync_all();   // the segment's barriers, Q, references and O'^T are free
             tc::fence_after_sync();
             if (*reinterpret_cast<volatile int *>(&s.abort)) break;
         }
     };
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
         segments([&](const Seg &sg) {
-            // ---------------- MMA issuer
-            if (warp == 1 && lane == 0) {
-                constexpr uint32_t id_s = tc::idesc_f16(kTile, N, false, false);
-                constexpr uint32_t id_o = tc::idesc_f16(kD, N, true, true);
-                auto issue_s = [&](int k) {   // tile k of the CTA
-                    const int st = k & 1;
-                    if (!wait(s, &s.k_full[st], (k >> 1) & 1)) return false;
-                    tc::fence_after_sync();
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        tc::mma_ts(tmem + kColS + st * N, tmem + kColK + st * 64 + kk * 8,
-                                   tc::sdesc_sw128(smem_addr(s.q[kk >> 2]) + (kk & 3) * 32, 16, 1024), id_s, kk > 0);
-                    tc::commit(&s.s_full[st]);
-                    tc::commit(&s.k_empty[st]);
-                    return true;
-                };
-                bool ok = issue_s(it);
-                for (int i = 0; ok && i < sg.n; ++i) {
+            if (warp == 0 || (warp == 2 && kTW == 2)) {
+                // ---------------- T [rows x quarters] = Q [z | s], 16-row tiles MT0 .. MT0 + MT - 1
+                constexpr int MT = N / 16 / kTW, MB = MT < 2 ? MT : 2;   // 16-row tiles of a warp, at a time
+                const float sc = a.scale_log2;
+                const int lrow = (lane & 7) + 8 * ((lane >> 3) & 1), lch = lane >> 4;
+                const uint32_t qrow = smem_addr(s.q[0]) + ((warp >> 1) * MT * 16 + lrow) * 128;
+                for (int i = 0; i < sg.n; ++i) {
                     const int k = it + i, st = k & 1;
-                    if (i + 1 < sg.n && !(ok = issue_s(k + 1))) break;
-                    ok = wait(s, &s.v_full[st], (k >> 1) & 1) && wait(s, &s.p_full[st], (k >> 1) & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
+                    const uint32_t keep = sg.x0 + i < a.nt_packed ? 0xffffffffu : 0u;   // fp16 tokens have no T
+                    // tz of two tiles ago has been read
+                    if (!wait_warp(s, &s.kz_full[st], ph(k)) || (k >= 2 && !wait_warp(s, &s.p_full[st], ph_prev(k)))) break;
+                    // column g_: z of quarter g_, then s of quarter g_ - 4
+                    const uint32_t *col = s.ksz[st][g_ & 3] + (g_ < 4 ? 64 : 0) + t_;
+                    float *tz = &s.tz[st][2 * (t_ & 1)][(warp >> 1) * MT * 16 + g_];
+#pragma unroll 1
+                    for (int m0 = 0; m0 < MT; m0 += MB) {
+                        float d[MB][2][4];
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        tc::mma_ss(tmem + kColO, tc::sdesc_sw128(smem_addr(s.v[st][0]) + kk * 2048, kTile * 128, 1024),
-                                   tc::sdesc_sw128(smem_addr(s.p[st][0]) + kk * 2048, kTile * 128, 1024), id_o,
-                                   (i > 0) || (kk > 0));
-                    tc::commit(&s.o_done[st]);
-                    tc::commit(&s.v_empty[st]);
+                        for (int e = 0; e < 8 * MB; ++e) (&d[0][0][0])[e] = 0.f;
+#pragma unroll 1
+                        for (int kb = 0; kb < 2; ++kb) {   // 64 channels: every load before the products
+                            uint32_t bz[4][2], qa[MB][4][4];
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                bz[kk][0] = col[32 * kb + 8 * kk] & keep;
+                                bz[kk][1] = col[32 * kb + 8 * kk + 4] & keep;
+#pragma unroll
+                                for (int m = 0; m < MB; ++m)
+                                    ldmatrix_x4(qa[m][kk], qrow + (m0 + m) * 2048 + kb * (N * 128) +
+                                                               (((2 * kk + lch) ^ (lrow & 7)) << 4));
+                            }
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                                for (int m = 0; m < MB; ++m) mma16816(d[m][kk & 1], qa[m][kk], bz[kk][0], bz[kk][1]);
+                        }
+#pragma unroll
+                        for (int m = 0; m < MB; ++m)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float v = d[m][0][e] + d[m][1][e];
+                                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                                if (t_ < 2) tz[(e & 1) * N + 16 * (m0 + m) + 8 * (e >> 1)] = v * sc;
+                            }
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::mbar_arrive(&s.t_full[st]);
+                        tc::mbar_arrive(&s.k_empty[st]);
+                    }
                 }
+            } else if (warp == 1) {
+                // ---------------- MMA issuer
+                if (lane == 0) {
+                    constexpr uint32_t id_s = tc::idesc_f16(kTile, N, false, false);
+                    constexpr uint32_t id_o = tc::idesc_f16(kD, N, true, true);
+                    auto issue_s = [&](int k) {   // tile k of the CTA
+                        const int st = k & 1;
+                        if (!wait(s, &s.k_full[st], ph(k))) return false;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            tc::mma_ts(tmem + kColS + st * N, tmem + kColK + st * 64 + kk * 8,
+                                       tc::sdesc_sw128(smem_addr(s.q[kk >> 2]) + (kk & 3) * 32, 16, 1024), id_s, kk > 0);
+                        tc::commit(&s.s_full[st]);
+                        tc::commit(&s.k_empty[st]);
+                        return true;
+                    };
+                    bool ok = issue_s(it);
+                    for (int i = 0; ok && i < sg.n; ++i) {
+                        const int k = it + i, st = k & 1;
+                        if (i + 1 < sg.n && !(ok = issue_s(k + 1))) break;
+                        ok = wait(s, &s.v_full[st], ph(k)) && wait(s, &s.p_full[st], ph(k));
+                        if (!ok) break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            tc::mma_ss(tmem + kColO, tc::sdesc_sw128(smem_addr(s.v[st][0]) + kk * 2048, kTile * 128, 1024),
+                                       tc::sdesc_sw128(smem_addr(s.p[st][0]) + kk * 2048, kTile * 128, 1024), id_o,
+                                       (i > 0) || (kk > 0));
+                        tc::commit(&s.o_done[st]);
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
         });
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
         segments([&](const Seg &sg) {
             // ---------------- K: token 32 quad + lane of the tile
             const size_t plane = (size_t)sg.kvh;
+            const Offset off(false);
             uint4 c0, c1;        // the token's codes
-            uint2 ks, kz;        // four channels of the warp's group: scale, zero
+            uint2 ks, kz;        // four channels of the quarter's group: scale, zero
             auto fetch = [&](int xt) {
                 const int t = xt * kTile + 32 * quad;   // the warp's first token: all 32 in one group
                 if (xt < a.nt_packed && t < a.n_packed) {
@@ -292,74 +417,76 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             for (int i = 0; i < sg.n; ++i) {
                 const int k = it + i, st = k & 1, xt = sg.x0 + i;
                 const bool packed = xt < a.nt_packed;
-                uint32_t *sz = s.ksz[quad][st];
+                uint32_t *sz = s.ksz[st][quad];
                 const int t = (packed ? xt : xt - a.nt_packed) * kTile + 32 * quad;
                 uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                if (packed) {
-                    // lanes of channels 16w + 0..7 pair the scales, those of 16w + 8..15 the zeros
-                    const bool up = lane & 2;
-                    const uint2 mine = up ? kz : ks, give = up ? ks : kz;
-                    uint2 got;
-                    got.x = __shfl_xor_sync(0xffffffffu, give.x, 2);
-                    got.y = __shfl_xor_sync(0xffffffffu, give.y, 2);
-                    const uint2 a0 = up ? got : mine, b0 = up ? mine : got;
-                    *reinterpret_cast<uint4 *>(sz + (up ? 64 : 0) + 8 * (lane >> 2) + 4 * (lane & 1)) =
-                        make_uint4(__byte_perm(a0.x, b0.x, 0x5410), __byte_perm(a0.x, b0.x, 0x7632),
-                                   __byte_perm(a0.y, b0.y, 0x5410), __byte_perm(a0.y, b0.y, 0x7632));
-                    __syncwarp();
-                }
+                // lanes of channels 16w + 0..7 pair the scales, those of 16w + 8..15 the zeros
+                const bool up = lane & 2;
+                const uint2 mine = up ? kz : ks, give = up ? ks : kz;
+                uint2 got;
+                got.x = __shfl_xor_sync(0xffffffffu, give.x, 2);
+                got.y = __shfl_xor_sync(0xffffffffu, give.y, 2);
+                const uint2 a0 = up ? got : mine, b0 = up ? mine : got;
                 fetch(xt + 1);
-                if (k >= 2 && !wait_warp(s, &s.k_empty[st], ((k >> 1) - 1) & 1)) break;
+                if (k >= 2 && !wait_warp(s, &s.k_empty[st], ph_prev(k))) break;
                 tc::fence_after_sync();
+                *reinterpret_cast<uint4 *>(sz + (up ? 64 : 0) + 8 * (lane >> 2) + 4 * (lane & 1)) =
+                    make_uint4(__byte_perm(a0.x, b0.x, 0x5410), __byte_perm(a0.x, b0.x, 0x7632),
+                               __byte_perm(a0.y, b0.y, 0x5410), __byte_perm(a0.y, b0.y, 0x7632));
+                arrive_warp(&s.kz_full[st]);
                 const uint32_t dst = tmem + lanes + kColK + st * 64;
-                if (packed) {
-                    const bool live = t < a.n_packed;
+                if (packed && t < a.n_packed) {
+                    uint32_t d = dst;
+                    const uint32_t *sp = sz;
+#pragma unroll 1
+                    for (int wi = 0; wi < 8; wi += 2, sp += 16, d += 16) {   // two words an iteration, then the next two move down
+                        uint4 sv4[4];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t out[32];
+                        for (int j = 0; j < 4; ++j) sv4[j] = *reinterpret_cast<const uint4 *>(sp + 4 * j);
+                        uint32_t out[16];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int wi = 4 * half + j;
-                            const uint4 s0 = *reinterpret_cast<const uint4 *>(sz + 8 * wi);
-                            const uint4 s1 = *reinterpret_cast<const uint4 *>(sz + 8 * wi + 4);
-                            const uint4 z0 = *reinterpret_cast<const uint4 *>(sz + 64 + 8 * wi);
-                            const uint4 z1 = *reinterpret_cast<const uint4 *>(sz + 64 + 8 * wi + 4);
+                        for (int j = 0; j < 2; ++j) {
+                            const uint4 s0 = sv4[2 * j], s1 = sv4[2 * j + 1];
                             const uint32_t sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-                            const uint32_t zv[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
-                            dequant_word(w[wi], [&](int i2) { return sv[i2]; }, [&](int i2) { return zv[i2]; }, out + 8 * j);
+                            dequant_word(w[j], off, [&](int i2) { return sv[i2]; }, out + 8 * j);
                         }
+                        tc::tmem_st<16>(d, out);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) out[j] = live ? out[j] : 0u;
-                        tc::tmem_st32(dst + 32 * half, out);
+                        for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
                     }
+                } else if (packed) {   // a quarter behind the last packed token
+                    uint32_t out[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) out[e] = 0u;
+#pragma unroll 1
+                    for (int wi = 0; wi < 4; ++wi) tc::tmem_st<16>(dst + 16 * wi, out);
                 } else {
                     const int i0 = t + lane;
                     int slot = a.res_start + i0;
                     if (slot >= a.ring) slot -= a.ring;
                     const uint4 *src =
                         reinterpret_cast<const uint4 *>(a.k_res + (plane * a.ring + (i0 < a.n_res ? slot : 0)) * kD);
+#pragma unroll 1
+                    for (int wi = 0; wi < 8; ++wi) {
+                        uint32_t out[8];
+                        pair_order(__ldg(src + 2 * wi), __ldg(src + 2 * wi + 1), out);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t out[32];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            pair_order(__ldg(src + 8 * half + 2 * j), __ldg(src + 8 * half + 2 * j + 1), out + 8 * j);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) out[j] = i0 < a.n_res ? out[j] : 0u;
-                        tc::tmem_st32(dst + 32 * half, out);
+                        for (int e = 0; e < 8; ++e) out[e] = i0 < a.n_res ? hmul2(out[e], kHalf2) : 0u;
+                        tc::tmem_st<8>(dst + 8 * wi, out);
                     }
                 }
                 tc::wait_st();
                 tc::fence_before_sync();
-                tc::mbar_arrive(&s.k_full[st]);
+                arrive_warp(&s.k_full[st]);
             }
         });
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         segments([&](const Seg &sg) {
             // ---------------- V: token 32 quad + lane of the tile
             const size_t plane = (size_t)sg.kvh;
             const int r = 32 * quad + lane;
+            const Offset off(lane & 1);
             uint4 c0, c1;
             uint32_t vs = 0, vz = 0;
             auto fetch = [&](int xt) {
@@ -377,95 +504,135 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 const int k = it + i, st = k & 1, xt = sg.x0 + i;
                 const bool packed = xt < a.nt_packed;
                 const int t = (packed ? xt : xt - a.nt_packed) * kTile + r;
-                const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                const uint32_t s2 = vs * 0x00010001u, z2 = vz * 0x00010001u;
-                fetch(xt + 1);
-                if (k >= 2 && !wait_warp(s, &s.v_empty[st], ((k >> 1) - 1) & 1)) break;
+                uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
                 const bool live = t < (packed ? a.n_packed : a.n_res);
-                int slot = a.res_start + t;
-                if (slot >= a.ring) slot -= a.ring;
-                const uint4 *src =
-                    reinterpret_cast<const uint4 *>(a.v_res + (plane * a.ring + (!packed && live ? slot : 0)) * kD);
+                // a token that is not there is zero everywhere: P = 0 must not meet garbage
+                const uint32_t s2 = vs * 0x00010001u;
+                const float zs = live && packed ? fmaf(lane & 1 ? 2.f : 1.f, h2f((uint16_t)vs), h2f((uint16_t)vz)) : 0.f;
+                const uint16_t zh = f2h(zs), zl = f2h(zs - h2f(zh));
+                fetch(xt + 1);
+                if (k >= 2 && !wait_warp(s, &s.o_done[st], ph_prev(k))) break;
+                reinterpret_cast<uint16_t *>(s.vz[st][0])[r] = zh;
+                reinterpret_cast<uint16_t *>(s.vz[st][1])[r] = zl;
+                unsigned char *row = reinterpret_cast<unsigned char *>(s.v[st][0]) + r * 128;
+                auto put = [&](int wi, const uint32_t *out) {   // the row's 16-byte chunks 2 wi, 2 wi + 1
+                    unsigned char *dst = row + (wi >> 2) * (kTile * 128);
+                    const int ch = (2 * (wi & 3)) ^ (r & 7);
+                    *reinterpret_cast<uint4 *>(dst + (ch << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+                    *reinterpret_cast<uint4 *>(dst + ((ch ^ 1) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+                };
+                if (packed && live) {   // (one answer a warp: the packed tokens are a multiple of 32)
+#pragma unroll 1
+                    for (int wi = 0; wi < 8; wi += 2) {
+                        uint32_t out[16];
+                        dequant_word(w[0], off, [&](int) { return s2; }, out);
+                        dequant_word(w[1], off, [&](int) { return s2; }, out + 8);
+                        put(wi, out);
+                        put(wi + 1, out + 8);
 #pragma unroll
-                for (int wi = 0; wi < 8; ++wi) {
-                    uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};   // a token that is not there: P = 0 must not meet garbage
-                    if (live) {
-                        if (packed) dequant_word(w[wi], [&](int) { return s2; }, [&](int) { return z2; }, out);
-                        else pair_order(__ldg(src + 2 * wi), __ldg(src + 2 * wi + 1), out);
+                        for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
                     }
-                    unsigned char *dst = reinterpret_cast<unsigned char *>(s.v[st][wi >> 2]) + r * 128;
-                    const int ch = 2 * (wi & 3);
-                    *reinterpret_cast<uint4 *>(dst + ((ch ^ (r & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
-                    *reinterpret_cast<uint4 *>(dst + (((ch + 1) ^ (r & 7)) << 4)) =
-                        make_uint4(out[4], out[5], out[6], out[7]);
+                } else if (packed) {
+                    const uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+                    for (int wi = 0; wi < 8; ++wi) put(wi, out);
+                } else {
+                    int slot = a.res_start + t;
+                    if (slot >= a.ring) slot -= a.ring;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(a.v_res + (plane * a.ring + (live ? slot : 0)) * kD);
+#pragma unroll 1
+                    for (int wi = 0; wi < 8; ++wi) {
+                        uint32_t out[8];
+                        pair_order(__ldg(src + 2 * wi), __ldg(src + 2 * wi + 1), out);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) out[e] = live ? hmul2(out[e], kHalf2) : 0u;
+                        put(wi, out);
+                    }
                 }
                 tc::fence_proxy_async_smem();
-                tc::mbar_arrive(&s.v_full[st]);
+                arrive_warp(&s.v_full[st]);
             }
         });
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 136;\n");
+    } else if (warp < 20) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
         segments([&](const Seg &sg) {
-            // ---------------- softmax: token lane r, columns n0 .. n0 + C - 1
+            // ---------------- softmax: token lane r, rows n0 .. n0 + C - 1
             const int half = warp >= 16, n0 = half * C, r = 32 * quad + lane, bar = 1 + half;
-            const int rank = r;   // of the 128 threads of the half
-            const float sc = a.scale_log2;
-            float l[C];
-#pragma unroll
-            for (int j = 0; j < C; ++j) l[j] = 0.f;
+            const float sc = 2.f * a.scale_log2;
+            float *bias = s.bias[warp - 12];
             bool ok = true;
             for (int i = 0; i < sg.n; ++i) {
                 const int k = it + i, st = k & 1, xt = sg.x0 + i;
                 const bool live = xt < a.nt_packed ? xt * kTile + r < a.n_packed
                                                    : (xt - a.nt_packed) * kTile + r < a.n_res;
-                ok = ok && wait_warp(s, &s.s_full[st], (k >> 1) & 1);
+                // T of the tile; P, alpha and the flag of two tiles ago have been read
+                ok = ok && wait_warp(s, &s.t_full[st], ph(k)) && (k < 2 || wait_warp(s, &s.o_done[st], ph_prev(k)));
+                for (int j = lane; j < C; j += 32) bias[j] = s.tz[st][quad][n0 + j] - s.m[n0 + j];
+                __syncwarp();
+                ok = ok && wait_warp(s, &s.s_full[st], ph(k));
                 tc::fence_after_sync();
                 const uint32_t ts = tmem + lanes + kColS + st * N + n0;
-                // does any score pass its row's reference by kLazy?
-                float mx = -INFINITY;
-#pragma unroll
-                for (int j0 = 0; j0 < C; j0 += CH) {
-                    uint32_t xr[CH];
-                    tc::tmem_ld<CH>(ts + j0, xr);
+                const unsigned long long sc2 = f2pack(sc, sc);
+                // the tile's log2 scores relative to the references; a second time if these move
+                // (C = 64: 32 at a time and read twice, so that the loop stays in the instruction cache)
+                float x[CH];
+                auto load = [&](int j0) {
+                    tc::tmem_ld<CH>(ts + j0, *reinterpret_cast<uint32_t(*)[CH]>(&x[0]));
                     tc::wait_ld();
 #pragma unroll
                     for (int j = 0; j < CH; j += 4) {
-                        const float4 m4 = *reinterpret_cast<const float4 *>(&s.m[n0 + j0 + j]);
-                        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(xr[j]), sc, -m4.x), fmaf(__uint_as_float(xr[j + 1]), sc, -m4.y)));
-                        mx = fmaxf(mx, fmaxf(fmaf(__uint_as_float(xr[j + 2]), sc, -m4.z), fmaf(__uint_as_float(xr[j + 3]), sc, -m4.w)));
+                        const float4 b4 = *reinterpret_cast<const float4 *>(&bias[j0 + j]);
+                        f2unpack(ffma2(f2pack(x[j], x[j + 1]), sc2, f2pack(b4.x, b4.y)), x[j], x[j + 1]);
+                        f2unpack(ffma2(f2pack(x[j + 2], x[j + 3]), sc2, f2pack(b4.z, b4.w)), x[j + 2], x[j + 3]);
                     }
-                }
-                // (a failed wait joins the vote: the warps of a half leave the loop together, at this barrier)
-                if (or_over(bar, !ok || (live && mx > kLazy))) {
+                };
+                bool moved = false, aborted = false;
+                for (;;) {
+                    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll 1
+                    for (int j0 = 0; j0 < C; j0 += CH) {
+                        load(j0);
+#pragma unroll
+                        for (int j = 0; j < CH; j += 4) {
+                            mx0 = max3(mx0, x[j], x[j + 1]);
+                            mx1 = max3(mx1, x[j + 2], x[j + 3]);
+                        }
+                    }
+                    // does a score pass its row's reference by kLazy?  (a failed wait joins the vote: the
+                    // warps of a half leave the loop together, at this barrier)
+                    if (moved || !or_over(bar, !ok || i == 0 || (live && fmaxf(mx0, mx1) > kLazy))) break;
+                    moved = true;
                     if (or_over(bar, !ok)) {
                         ok = false;
+                        aborted = true;
                         break;
                     }
-                    // column maxima of the tile -> new references; sums and O^T follow
+                    // column maxima of the tile -> new references; the sums and O'^T follow
 #pragma unroll 1
-                    for (int j = 0; j < C; j += 8) {
-                        uint32_t xr[8];
-                        tc::tmem_ld<8>(ts + j, xr);
+                    for (int j0 = 0; j0 < C; j0 += 8) {
+                        uint32_t y[8];
+                        tc::tmem_ld<8>(ts + j0, y);
                         tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float top = warp_max(live ? __uint_as_float(xr[e]) : -INFINITY);
-                            if (lane == 0) s.wmax[quad][n0 + j + e] = top;
+                        for (int j = 0; j < 8; ++j) {
+                            const float top = warp_max(live ? fmaf(__uint_as_float(y[j]), sc, bias[j0 + j]) : -INFINITY);
+                            if (lane == j) s.wmax[quad][n0 + j0 + j] = top;
                         }
                     }
                     sync_half(bar);
-                    if (rank < C) {
-                        const int n = n0 + rank;
-                        const float top = fmaxf(fmaxf(s.wmax[0][n], s.wmax[1][n]), fmaxf(s.wmax[2][n], s.wmax[3][n])) * sc;
-                        const float old = s.m[n], now = fmaxf(old, top);
-                        s.m[n] = now;
-                        s.alpha[n] = ex2(old - now);
+                    if (r < C) {
+                        const int n = n0 + r;
+                        const float top = fmaxf(fmaxf(s.wmax[0][n], s.wmax[1][n]), fmaxf(s.wmax[2][n], s.wmax[3][n]));
+                        // how far the reference moves; the first tile's maximum sets it
+                        const float up = i > 0 ? fmaxf(top, 0.f) : top == -INFINITY ? 0.f : top;
+                        s.m[n] += up;
+                        s.alpha[st][n] = i > 0 ? ex2(-up) : 1.f;
                     }
                     sync_half(bar);
-#pragma unroll
-                    for (int j = 0; j < C; ++j) l[j] *= s.alpha[n0 + j];
+                    for (int j = lane; j < C; j += 32) bias[j] = s.tz[st][quad][n0 + j] - s.m[n0 + j];
+                    __syncwarp();
                     if (i > 0) {
-                        ok = wait_warp(s, &s.o_done[(k - 1) & 1], ((k - 1) >> 1) & 1);
+                        ok = wait_warp(s, &s.o_done[(k - 1) & 1], ph(k - 1));
                         tc::fence_after_sync();
                         const uint32_t to = tmem + lanes + kColO + n0;
 #pragma unroll 1
@@ -474,67 +641,40 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                             tc::tmem_ld<8>(to + j, o);
                             tc::wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s.alpha[n0 + j + e]);
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * s.alpha[st][n0 + j + e]);
                             tc::tmem_st<8>(to + j, o);
                         }
                         tc::wait_st();
                     }
                 }
-                // P of two tiles ago has been read
-                if (k >= 2) ok = ok && wait_warp(s, &s.o_done[st], ((k >> 1) - 1) & 1);
-                if (!ok) continue;   // to the next tile's vote, or the epilogue
-#pragma unroll
+                if (!ok) {
+                    if (aborted) break;
+                    continue;   // to the next tile's vote, or the epilogue
+                }
+                if (r == 0) s.resc[st][half] = moved;
+                const uint32_t live2 = live ? 0xffffffffu : 0u;
+                unsigned char *row = reinterpret_cast<unsigned char *>(s.p[st][n0 >> 6]) + r * 128;
+#pragma unroll 1
                 for (int j0 = 0; j0 < C; j0 += CH) {
-                    uint32_t xr[CH];
-                    tc::tmem_ld<CH>(ts + j0, xr);
-                    tc::wait_ld();
+                    if (C > CH) load(j0);
 #pragma unroll
                     for (int j = 0; j < CH; j += 8) {
-                        uint32_t ph[4];
+                        uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 8; e += 4) {
-                            const float4 m4 = *reinterpret_cast<const float4 *>(&s.m[n0 + j0 + j + e]);
-                            const float p0 = live ? ex2(fmaf(__uint_as_float(xr[j + e]), sc, -m4.x)) : 0.f;
-                            const float p1 = live ? ex2(fmaf(__uint_as_float(xr[j + e + 1]), sc, -m4.y)) : 0.f;
-                            const float p2 = live ? ex2(fmaf(__uint_as_float(xr[j + e + 2]), sc, -m4.z)) : 0.f;
-                            const float p3 = live ? ex2(fmaf(__uint_as_float(xr[j + e + 3]), sc, -m4.w)) : 0.f;
-                            l[j0 + j + e] += p0;
-                            l[j0 + j + e + 1] += p1;
-                            l[j0 + j + e + 2] += p2;
-                            l[j0 + j + e + 3] += p3;
-                            ph[e / 2] = pack_half2(p0, p1);
-                            ph[e / 2 + 1] = pack_half2(p2, p3);
-                        }
-                        const int n = n0 + j0 + j, blkn = n >> 6, ch = (n & 63) >> 3;
-                        *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(s.p[st][blkn]) + r * 128 +
-                                                   ((ch ^ (r & 7)) << 4)) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                        for (int e = 0; e < 4; ++e) w[e] = pack_half2(ex2(x[j + 2 * e]), ex2(x[j + 2 * e + 1])) & live2;
+                        *reinterpret_cast<uint4 *>(row + (((((n0 + j0 + j) & 63) >> 3) ^ (r & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 tc::fence_proxy_async_smem();
                 tc::fence_before_sync();
-                tc::mbar_arrive(&s.p_full[st]);
+                arrive_warp(&s.p_full[st]);
             }
             // ---------------- epilogue: the segment's state to slot c + u
             const int last = it + sg.n - 1;
-            if (ok) ok = wait_warp(s, &s.o_done[last & 1], (last >> 1) & 1);
-            // sums over the 32 lanes: column j of a block of CH ends in lanes j (mod CH)
-#pragma unroll
-            for (int j0 = 0; j0 < C; j0 += CH) {
-#pragma unroll
-                for (int w = CH / 2; w >= 1; w >>= 1) {
-                    const bool up = lane & w;
-#pragma unroll
-                    for (int j = 0; j < w; ++j) {
-                        const float keep = up ? l[j0 + j + w] : l[j0 + j], give = up ? l[j0 + j] : l[j0 + j + w];
-                        l[j0 + j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
-                    }
-                }
-                float t = l[j0];
-#pragma unroll
-                for (int w = CH; w < 32; w <<= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
-                if (lane < CH) s.wsum[quad][n0 + j0 + lane] = t;
-            }
-            sync_half(bar);
+            if (ok) ok = wait_warp(s, &s.o_done[last & 1], ph(last));
+            asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(3 + half), "n"(128 + 16 * kSW) : "memory");   // the sums are in s.l, s.pz
             if (ok) {
                 tc::fence_after_sync();
                 float *base = a.part + (size_t)(c + sg.u) * N * kPreStride;
@@ -548,15 +688,89 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     tc::wait_ld();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        if (j + e < rows) base[(size_t)(n0 + j + e) * kPreStride + ch] = __uint_as_float(o[e]);
+                        if (j + e < rows)
+                            base[(size_t)(n0 + j + e) * kPreStride + ch] = fmaf(2.f, __uint_as_float(o[e]), s.pz[n0 + j + e]);
                 }
-                if (rank < rows) {
-                    const int n = n0 + rank;
+                if (r < rows) {
+                    const int n = n0 + r;
                     base[(size_t)n * kPreStride + 128] = s.m[n];
-                    base[(size_t)n * kPreStride + 129] = s.wsum[0][n] + s.wsum[1][n] + s.wsum[2][n] + s.wsum[3][n];
+                    base[(size_t)n * kPreStride + 129] = s.l[n];
                 }
             }
             tc::fence_before_sync();
+        });
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+        segments([&](const Seg &sg) {
+            // ---------------- sums over P: [1; hi; lo] P, rows g_ = 0, 1, 2 of the product, for rows n0 .. n0 + 8 NT - 1
+            constexpr int NT = N / 8 / kSW;   // 8-row tiles of a warp
+            constexpr int KB = NT < 2 ? 8 : 16 / NT;   // 16-token steps whose loads go out together
+            if (quad < kSW) {
+                const int n0 = quad * NT * 8, half = quad / (kSW / 2);
+                float total[NT][2];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) total[j][0] = total[j][1] = 0.f;
+                // ldmatrix rows: token (lane & 15) of a 16-token step; columns: an 8-row chunk of P (lanes
+                // 16-31 the next one; with one chunk in all the same one again)
+                const int trow = lane & 15, ch0 = ((n0 & 63) >> 3) + (NT > 1 ? lane >> 4 : 0);
+                for (int i = 0; i < sg.n; ++i) {
+                    const int k = it + i, st = k & 1;
+                    if (!wait_warp(s, &s.v_full[st], ph(k)) || !wait_warp(s, &s.p_full[st], ph(k))) break;
+                    if (s.resc[st][half]) {
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const float2 al = *reinterpret_cast<const float2 *>(&s.alpha[st][n0 + 8 * j + 2 * t_]);
+                            total[j][0] *= al.x;
+                            total[j][1] *= al.y;
+                        }
+                    }
+                    float d[NT][4];   // this tile's sums (a long sum stays in fp32 additions)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
+                    const uint32_t *zrow = s.vz[st][g_ == 2] + t_;
+                    const uint32_t one = g_ == 0 ? 0x3C003C00u : 0u, zmask = g_ == 1 || g_ == 2 ? 0xffffffffu : 0u;
+                    const uint32_t prow = smem_addr(s.p[st][n0 >> 6]) + trow * 128;
+#pragma unroll 1
+                    for (int k0 = 0; k0 < 8; k0 += KB) {
+                        uint32_t af[KB][2], b[KB][(NT + 1) / 2][4];
+#pragma unroll
+                        for (int e = 0; e < KB; ++e) {
+                            af[e][0] = (zrow[8 * (k0 + e)] & zmask) | one;
+                            af[e][1] = (zrow[8 * (k0 + e) + 4] & zmask) | one;
+#pragma unroll
+                            for (int j = 0; j < NT; j += 2)
+                                ldmatrix_x4_t(b[e][j / 2], prow + (k0 + e) * 2048 + (((ch0 + j) ^ (trow & 7)) << 4));
+                        }
+#pragma unroll
+                        for (int e = 0; e < KB; ++e) {
+                            const uint32_t a4[4] = {af[e][0], 0u, af[e][1], 0u};
+#pragma unroll
+                            for (int j = 0; j < NT; j += 2) {
+                                mma16816(d[j], a4, b[e][j / 2][0], b[e][j / 2][1]);
+                                if (NT > 1) mma16816(d[j + (NT > 1)], a4, b[e][j / 2][2], b[e][j / 2][3]);
+                            }
+                        }
+                    }
+                    arrive_warp(&s.o_done[st]);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        total[j][0] += d[j][0];
+                        total[j][1] += d[j][1];
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float lo_part = __shfl_down_sync(0xffffffffu, total[j][e], 4);   // row g_ + 1
+                        const int n = n0 + 8 * j + 2 * t_ + e;
+                        if (g_ == 0) s.l[n] = total[j][e];
+                        if (g_ == 1) s.pz[n] = total[j][e] + lo_part;
+                    }
+                }
+                __syncwarp();
+                asm volatile("barrier.cta.arrive %0, %1;\n" ::"r"(3 + half), "n"(128 + 16 * kSW) : "memory");   // to the half's epilogue
+            }
         });
     }
     if (warp == 1) {
