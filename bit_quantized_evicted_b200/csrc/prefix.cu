@@ -35,8 +35,8 @@
 // The loops are kept short on purpose: with the five roles unrolled over their
 // tiles, 7.7 of 14 warps waited for instructions (N = 64; 3.3 us a tile).
 //
-// 24 warps: 0 and 2 compute T (half of the rows each), 1 issues the MMAs, 4-7
-// dequantize K, 8-11 V (a thread a token), 12-19 softmax (thread = token lane,
+// 24 warps: 0 and 2 compute T (half of the rows each), 1 and 3 issue the
+// MMAs of the two products, 4-7 dequantize K, 8-11 V (a thread a token), 12-19 softmax (thread = token lane,
 // half of the rows each), 20-23 the sums over P (a quarter of the rows each).  S, K', V' and P have two
 // buffers.  The reference max of a row moves only when a score passes it by 2^8;
 // then the column maxima of a half's four warps meet in shared memory and O'^T
@@ -56,6 +56,8 @@ namespace {
 constexpr int kTile = 128;      // tokens of a tile
 constexpr int kThreads = 768;
 constexpr float kLazy = 8.f;
+// words of a quarter's scales and zeros: the eight columns that T reads side by side lie in distinct banks
+constexpr int kKszZero = 68, kKszStride = 136;
 
 template <int N>
 struct Smem {
@@ -63,14 +65,14 @@ struct Smem {
     uint16_t v[2][2][kTile * 64];       // [stage][64-channel block][token][64], 128-byte swizzle
     uint16_t p[2][kNB][kTile * 64];     // [stage][64-row block][token][64]
     uint16_t q[2][N * 64];              // [64-channel block][row][64]
-    uint32_t ksz[2][4][128];            // [stage][quarter]: scale pairs [64], zero pairs [64] of its key group
+    uint32_t ksz[2][4][kKszStride];     // [stage][quarter]: scale pairs [64], zero pairs [64] of its key group
     uint32_t vz[2][2][kTile / 2];       // [stage][hi, lo]: fp16 z + o s of the value tokens
     float tz[2][4][N];                  // [stage][quarter][row]: T in log2 units
     float bias[8][N / 2];               // a softmax warp's T - reference of the tile in hand
     float m[N], alpha[2][N], l[N], pz[N];
     float wmax[4][N];
     int resc[2][2];                     // [stage][half]: the tile moved the references (alpha holds the factors)
-    uint64_t k_full[2], k_empty[2], kz_full[2], t_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain;
+    uint64_t k_full[2], k_empty[2], kz_full[2], t_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain[2];
     uint32_t tmem_base;
     int abort;
 };
@@ -88,48 +90,9 @@ struct Args {
     short seq[MINIKV_MAX_RAGGED_SEQS];   // listed: sequence of each place
 };
 
-// Polls before a wait gives up; each may suspend the thread for kSuspendNs (4 s in all).
-#ifndef MINIKV_WAIT_LIMIT
-#define MINIKV_WAIT_LIMIT (1u << 18)
-#endif
-constexpr uint32_t kSuspendNs = 16384;
-
-// Bounded waits of the CTA: once one gives up, every wait that is not already
-// over returns false, so all roles reach the segment's end.  The common case, a
-// phase that is over, takes a handful of instructions: twenty warps in five
-// roles share the instruction caches.
-// up to n polls
-__device__ __forceinline__ uint32_t poll(uint64_t *bar, uint32_t parity, uint32_t n) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p, q;\n .reg .b32 n;\n mov.b32 n, %4;\n"
-        "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n @p bra OVER;\n"
-        " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra POLL;\n"
-        "OVER:\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done) : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendNs), "r"(n) : "memory");
-    return done;
-}
-constexpr uint32_t kPolls = MINIKV_WAIT_LIMIT < 256 ? MINIKV_WAIT_LIMIT : 256;   // between two looks at the abort flag
 template <class S>
-__device__ __forceinline__ bool wait(S &s, uint64_t *bar, uint32_t parity) {   // one thread
-    for (uint32_t i = 0; !poll(bar, parity, kPolls); i += kPolls) {
-        if (i + kPolls >= MINIKV_WAIT_LIMIT) *reinterpret_cast<volatile int *>(&s.abort) = 1;
-        if (*reinterpret_cast<volatile int *>(&s.abort)) return false;
-    }
-    return true;
-}
-template <class S>
-__device__ __forceinline__ bool wait_warp(S &s, uint64_t *bar, uint32_t parity) {   // a warp's 32 lanes
-    for (uint32_t i = 0; !__all_sync(0xffffffffu, poll(bar, parity, kPolls)); i += kPolls) {
-        if (i + kPolls >= MINIKV_WAIT_LIMIT) *reinterpret_cast<volatile int *>(&s.abort) = 1;
-        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&s.abort))) return false;
-    }
-    return true;
-}
-// The warp's arrival, once all its lanes are here.
-__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+__device__ __forceinline__ bool wait_warp(S &s, uint64_t *bar, uint32_t parity) {
+    return tc::role_wait_warp(&s.abort, bar, parity);
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -249,7 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     using S = Smem<N>;
     S &s = *reinterpret_cast<S *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = warp & 3;
+    // (broadcast: the compiler then knows that branches on the warp, and descriptors behind them, are uniform)
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), quad = warp & 3;
     const int g_ = lane >> 2, t_ = lane & 3;
     const int c = blockIdx.x;
 
@@ -262,10 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             mbar_init(&s.t_full[i], kTW);
             mbar_init(&s.v_full[i], 4);
             mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.drain[i], 1);
             mbar_init(&s.p_full[i], 8);
             mbar_init(&s.o_done[i], 1 + kSW);    // O'^T has the tile; the sum warps have its sums
         }
-        mbar_init(&s.drain, 1);
         s.abort = 0;
         fence_mbar_init();
     }
@@ -274,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = s.tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem_base, 0);
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
 
     const int lo = (int)((long long)c * a.tab.T / a.tab.P), hi = (int)((long long)(c + 1) * a.tab.T / a.tab.P);
@@ -320,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     // tz of two tiles ago has been read
                     if (!wait_warp(s, &s.kz_full[st], ph(k)) || (k >= 2 && !wait_warp(s, &s.p_full[st], ph_prev(k)))) break;
                     // column g_: z of quarter g_, then s of quarter g_ - 4
-                    const uint32_t *col = s.ksz[st][g_ & 3] + (g_ < 4 ? 64 : 0) + t_;
+                    const uint32_t *col = s.ksz[st][g_ & 3] + (g_ < 4 ? kKszZero : 0) + t_;
                     float *tz = &s.tz[st][2 * (t_ & 1)][(warp >> 1) * MT * 16 + g_];
 #pragma unroll 1
                     for (int m0 = 0; m0 < MT; m0 += MB) {
@@ -360,38 +324,44 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     }
                 }
             } else if (warp == 1) {
-                // ---------------- MMA issuer
-                if (lane == 0) {
-                    constexpr uint32_t id_s = tc::idesc_f16(kTile, N, false, false);
-                    constexpr uint32_t id_o = tc::idesc_f16(kD, N, true, true);
-                    auto issue_s = [&](int k) {   // tile k of the CTA
-                        const int st = k & 1;
-                        if (!wait(s, &s.k_full[st], ph(k))) return false;
-                        tc::fence_after_sync();
+                // ---------------- S'^T = K' Q^T (the warp waits together, one lane issues)
+                constexpr uint32_t id_s = tc::idesc_f16(kTile, N, false, false);
+                const uint64_t qd = tc::sdesc_sw128(smem_addr(s.q[0]), 16, 1024);
+                for (int i = 0; i < sg.n; ++i) {
+                    const int k = it + i;
+                    const uint32_t st = k & 1;
+                    // S of two tiles ago has been read
+                    if (!wait_warp(s, &s.k_full[st], ph(k)) || (k >= 2 && !wait_warp(s, &s.p_full[st], ph_prev(k)))) break;
+                    tc::fence_after_sync();
+                    if (tc::elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
+                        for (int kk = 0; kk < 8; ++kk)   // descriptors count 16-byte units
                             tc::mma_ts(tmem + kColS + st * N, tmem + kColK + st * 64 + kk * 8,
-                                       tc::sdesc_sw128(smem_addr(s.q[kk >> 2]) + (kk & 3) * 32, 16, 1024), id_s, kk > 0);
+                                       qd + (kk >> 2) * (N * 8) + (kk & 3) * 2, id_s, kk > 0);
                         tc::commit(&s.s_full[st]);
                         tc::commit(&s.k_empty[st]);
-                        return true;
-                    };
-                    bool ok = issue_s(it);
-                    for (int i = 0; ok && i < sg.n; ++i) {
-                        const int k = it + i, st = k & 1;
-                        if (i + 1 < sg.n && !(ok = issue_s(k + 1))) break;
-                        ok = wait(s, &s.v_full[st], ph(k)) && wait(s, &s.p_full[st], ph(k));
-                        if (!ok) break;
-                        tc::fence_after_sync();
+                    }
+                    __syncwarp();
+                }
+            } else if (warp == 3) {
+                // ---------------- O'^T += V'^T P^T
+                constexpr uint32_t id_o = tc::idesc_f16(kD, N, true, true);
+                const uint64_t vd = tc::sdesc_sw128(smem_addr(s.v[0][0]), kTile * 128, 1024);
+                const uint64_t pd = tc::sdesc_sw128(smem_addr(s.p[0][0]), kTile * 128, 1024);
+                for (int i = 0; i < sg.n; ++i) {
+                    const int k = it + i;
+                    const uint32_t st = k & 1;
+                    if (!wait_warp(s, &s.v_full[st], ph(k)) || !wait_warp(s, &s.p_full[st], ph(k))) break;
+                    tc::fence_after_sync();
+                    if (tc::elect_one()) {
+                        const uint64_t v = vd + st * (2 * kTile * 8), p = pd + st * (S::kNB * kTile * 8);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            tc::mma_ss(tmem + kColO, tc::sdesc_sw128(smem_addr(s.v[st][0]) + kk * 2048, kTile * 128, 1024),
-                                       tc::sdesc_sw128(smem_addr(s.p[st][0]) + kk * 2048, kTile * 128, 1024), id_o,
-                                       (i > 0) || (kk > 0));
+                            tc::mma_ss(tmem + kColO, v + kk * 128, p + kk * 128, id_o, (i > 0) || (kk > 0));
                         tc::commit(&s.o_done[st]);
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         });
     } else if (warp < 8) {
@@ -430,10 +400,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 fetch(xt + 1);
                 if (k >= 2 && !wait_warp(s, &s.k_empty[st], ph_prev(k))) break;
                 tc::fence_after_sync();
-                *reinterpret_cast<uint4 *>(sz + (up ? 64 : 0) + 8 * (lane >> 2) + 4 * (lane & 1)) =
+                *reinterpret_cast<uint4 *>(sz + (up ? kKszZero : 0) + 8 * (lane >> 2) + 4 * (lane & 1)) =
                     make_uint4(__byte_perm(a0.x, b0.x, 0x5410), __byte_perm(a0.x, b0.x, 0x7632),
                                __byte_perm(a0.y, b0.y, 0x5410), __byte_perm(a0.y, b0.y, 0x7632));
-                arrive_warp(&s.kz_full[st]);
+                tc::arrive_warp(&s.kz_full[st]);
                 const uint32_t dst = tmem + lanes + kColK + st * 64;
                 if (packed && t < a.n_packed) {
                     uint32_t d = dst;
@@ -477,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 }
                 tc::wait_st();
                 tc::fence_before_sync();
-                arrive_warp(&s.k_full[st]);
+                tc::arrive_warp(&s.k_full[st]);
             }
         });
     } else if (warp < 12) {
@@ -550,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     }
                 }
                 tc::fence_proxy_async_smem();
-                arrive_warp(&s.v_full[st]);
+                tc::arrive_warp(&s.v_full[st]);
             }
         });
     } else if (warp < 20) {
@@ -669,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 }
                 tc::fence_proxy_async_smem();
                 tc::fence_before_sync();
-                arrive_warp(&s.p_full[st]);
+                tc::arrive_warp(&s.p_full[st]);
             }
             // ---------------- epilogue: the segment's state to slot c + u
             const int last = it + sg.n - 1;
@@ -751,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                             }
                         }
                     }
-                    arrive_warp(&s.o_done[st]);
+                    tc::arrive_warp(&s.o_done[st]);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         total[j][0] += d[j][0];
@@ -773,14 +743,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             }
         });
     }
-    if (warp == 1) {
-        if (lane == 0) {   // every MMA issued has finished (after an expired wait, too)
-            tc::commit(&s.drain);
-            mbar_wait(&s.drain, 0);
-        }
+    if (warp == 1 || warp == 3) {   // every MMA issued has finished (after an expired wait, too)
+        if (tc::elect_one()) tc::commit(&s.drain[warp >> 1]);
         __syncwarp();
-        tc::tmem_dealloc(tmem, kCols);
+        mbar_wait(&s.drain[warp >> 1], 0);
     }
+    __syncthreads();
+    if (warp == 1) tc::tmem_dealloc(tmem, kCols);
     if (tid == 0) a.status[c] = s.abort ? 1u : 0u;
 }
 

@@ -129,6 +129,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u));
 }
+// One lane of the warp, the same at every call; the compiler knows that a branch
+// on it has one thread, and keeps descriptors in uniform registers there (behind
+// `lane == 0` an MMA took 46 cycles to issue, behind this at most 32).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+    return p != 0;
+}
 // The mbarrier arrives once every tcgen05 operation this thread issued before has completed.
 __device__ __forceinline__ void commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(
@@ -167,6 +175,53 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// ---- bounded waits of a CTA's roles -----------------------------------------------
+
+// Polls before a wait gives up; each may suspend the thread for kSuspendNs (4 s in all).
+#ifndef MINIKV_ROLE_WAIT_LIMIT
+#define MINIKV_ROLE_WAIT_LIMIT (1u << 18)
+#endif
+constexpr uint32_t kSuspendNs = 16384;
+
+// Once a wait gives up (it sets *abort, in shared memory), every wait of the CTA
+// that is not already over returns false, so all roles reach the CTA's end.  The
+// common case, a phase that is over, is one poll and a branch: under a running
+// MMA every shared-memory access takes hundreds of cycles (looking at the abort
+// flag first doubled a wait that was over, to 300-400), and in kernels of many
+// roles the instruction caches are short.
+// up to n polls
+__device__ __forceinline__ uint32_t poll(uint64_t *bar, uint32_t parity, uint32_t n) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b32 n;\n mov.b32 n, %4;\n"
+        "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n @p bra OVER;\n"
+        " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra POLL;\n"
+        "OVER:\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done) : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendNs), "r"(n) : "memory");
+    return done;
+}
+constexpr uint32_t kPolls = MINIKV_ROLE_WAIT_LIMIT < 256 ? MINIKV_ROLE_WAIT_LIMIT : 256;   // between two looks at *abort
+__device__ __forceinline__ bool role_wait(int *abort, uint64_t *bar, uint32_t parity) {   // one thread
+    for (uint32_t i = 0; !poll(bar, parity, kPolls); i += kPolls) {
+        if (i + kPolls >= MINIKV_ROLE_WAIT_LIMIT) *reinterpret_cast<volatile int *>(abort) = 1;
+        if (*reinterpret_cast<volatile int *>(abort)) return false;
+    }
+    return true;
+}
+__device__ __forceinline__ bool role_wait_warp(int *abort, uint64_t *bar, uint32_t parity) {   // a warp's 32 lanes
+    for (uint32_t i = 0; !__all_sync(0xffffffffu, poll(bar, parity, kPolls)); i += kPolls) {
+        if (i + kPolls >= MINIKV_ROLE_WAIT_LIMIT) *reinterpret_cast<volatile int *>(abort) = 1;
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(abort))) return false;
+    }
+    return true;
+}
+// The warp's arrival, once all its lanes are here (32 lanes' arrivals would be
+// served one after another).
+__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 }  // namespace tc

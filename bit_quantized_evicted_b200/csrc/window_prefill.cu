@@ -10,16 +10,19 @@
 // block between two heads at the same positions.  12 warps:
 //   warp 0      TMA producer: both Q tiles, then K_0, V_0, K_1, V_1, .. into a
 //               ring of 5 x 32 KB;
-//   warp 1      TMEM owner and the single thread issuing tcgen05.mma;
+//   warp 1      TMEM owner;
+//   warps 2, 3  issue tcgen05.mma, a warp a query tile;
 //   warps 4-7   softmax of tile 0, warps 8-11 of tile 1: thread = query row =
 //               TMEM lane; also the rescale of O and the epilogue.
 // Tensor memory (all 512 columns): S_0, S_1, O_0, O_1 fp32 [128 x 128].  P_t
 // (fp16 pairs, 64 columns) takes the place of S_t once the row is in registers.
-// Issue order: S_0(0), S_1(0), then for every block j and tile t in turn
-// P_t V(j), S_t(j+1): while a tile's softmax works, the tensor cores have the
-// other tile's two products.  A commit covers everything issued before it, so
-// S_t(j+1) complete means O_t holds block j: the softmax may rescale O_t.
-// tcgen05.mma of one thread run in issue order, so S_t(j+1) over P_t(j) is safe.
+// Issue order of tile t: S(0), then for every block j P V(j), S(j+1): while a
+// tile's softmax works, the tensor cores have the other tile's two products.
+// One warp issuing for both tiles left the pipe idle during its waits (about 250
+// cycles each under running MMAs, 1100 of 4400 a block pair).  A commit covers
+// everything its thread issued before it, so S_t(j+1) complete means O_t holds
+// block j: the softmax may rescale O_t.  tcgen05.mma of one thread run in issue
+// order, so S_t(j+1) over P_t(j) is safe.
 //
 // Softmax: base 2, running reference max that moves only when a score passes it
 // by 2^8 (p <= 256 keeps its 11 bits in fp16; O is rescaled rarely).  P is
@@ -53,9 +56,10 @@ constexpr float kNone = -1e30f;             // reference max of a row that has s
 struct Smem {
     uint16_t q[2][2][kM * 64];       // [tile][64-wide d block], 128-byte swizzle
     uint16_t kv[kRing][2][kN * 64];
-    uint64_t q_full, full[kRing], empty[kRing];
+    uint64_t q_full, full[kRing];
+    uint64_t done[2];                // step 0, S(0), and j + 1, P V(j) and S(j + 1), of both tiles have read their blocks
     uint64_t s_full[2], p_full[2], o_done[2];
-    uint64_t drain;
+    uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
     int slow[2];                     // tile t met an infinity or NaN in a partly visible V block
@@ -69,15 +73,8 @@ struct Args {
     float scale_log2;
 };
 
-#ifndef MINIKV_WAIT_LIMIT
-#define MINIKV_WAIT_LIMIT (1u << 26)
-#endif
-
-__device__ __forceinline__ bool wait(Smem &s, uint64_t *bar, uint32_t parity) {
-    if (*reinterpret_cast<volatile int *>(&s.abort)) return false;
-    if (mbar_wait(bar, parity, MINIKV_WAIT_LIMIT)) return true;
-    *reinterpret_cast<volatile int *>(&s.abort) = 1;
-    return false;
+__device__ __forceinline__ bool wait_warp(Smem &s, uint64_t *bar, uint32_t parity) {
+    return tc::role_wait_warp(&s.abort, bar, parity);
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -174,7 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ Args a) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     Smem &s = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // (broadcast: the compiler then knows that branches on the warp, and descriptors behind them, are uniform)
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
     // the pairs with the longest bands first, all units side by side: their K / V bands overlap in L2
     const int pair = a.npair - 1 - (int)blockIdx.x / a.units, unit = (int)blockIdx.x % a.units;
@@ -186,17 +184,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         mbar_init(&s.q_full, 1);
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], 1);
-        }
+        for (int i = 0; i < kRing; ++i) mbar_init(&s.full[i], 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s.s_full[t], 1);
-            mbar_init(&s.p_full[t], 128);
+            mbar_init(&s.done[t], 2);     // both issuers
+            mbar_init(&s.drain[t], 1);
+            mbar_init(&s.p_full[t], 4);   // warps
             mbar_init(&s.o_done[t], 1);
             s.slow[t] = 0;
         }
-        mbar_init(&s.drain, 1);
         s.abort = 0;
         fence_mbar_init();
     }
@@ -204,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = s.tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s.tmem_base, 0);
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
@@ -219,69 +215,72 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tma_load_3d(s.q[t][0], &map_q, 0, ti.q0, b * a.Hq + ti.h, &s.q_full);
                 tc::tma_load_3d(s.q[t][1], &map_q, 64, ti.q0, b * a.Hq + ti.h, &s.q_full);
             }
+            // K_j and V_j take the slots of V_{j-3} and K_{j-2}, both free after step j - 2 (of the two barriers that
+            // count steps, the one waited on moves again with step j, which needs K_j)
             int issued = 0;
-            for (int e = 0; e < 2 * blk.n; ++e) {
-                const int st = e % kRing;
-                if (e >= kRing && !wait(s, &s.empty[st], (e / kRing - 1) & 1)) break;
-                const CUtensorMap *m = e & 1 ? &map_v : &map_k;
-                const int row = blk.at(e >> 1) * kN;
-                mbar_arrive_expect_tx(&s.full[st], 2 * kN * 128);
-                tc::tma_load_3d(s.kv[st][0], m, 0, row, unit, &s.full[st]);
-                tc::tma_load_3d(s.kv[st][1], m, 64, row, unit, &s.full[st]);
-                issued = e + 1;
+            for (int j = 0; j < blk.n; ++j) {
+                if (j >= 2 && !tc::role_wait(&s.abort, &s.done[j & 1], ((j - 2) >> 1) & 1)) break;
+                const int row = blk.at(j) * kN;
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const int st = (2 * j + v) % kRing;
+                    const CUtensorMap *m = v ? &map_v : &map_k;
+                    mbar_arrive_expect_tx(&s.full[st], 2 * kN * 128);
+                    tc::tma_load_3d(s.kv[st][0], m, 0, row, unit, &s.full[st]);
+                    tc::tma_load_3d(s.kv[st][1], m, 64, row, unit, &s.full[st]);
+                }
+                issued = 2 * j + 2;
             }
             if (*reinterpret_cast<volatile int *>(&s.abort)) {   // let the loads queued here land before the CTA exits
                 mbar_wait(&s.q_full, 0);
                 for (int e = issued > kRing ? issued - kRing : 0; e < issued; ++e)
                     mbar_wait(&s.full[e % kRing], (e / kRing) & 1);
             }
-        } else if (warp == 1 && lane == 0) {
-            // ---------------- MMA issuer
+        } else if (warp >= 2) {
+            // ---------------- MMA issuer of tile t (the warp waits together, one lane issues)
+            const int t = warp - 2;
             constexpr uint32_t id_s = tc::idesc_f16(kM, kN, false, false);
             constexpr uint32_t id_pv = tc::idesc_f16(kM, kD, false, true);
-            auto full = [&](int e) { return wait(s, &s.full[e % kRing], (e / kRing) & 1); };
-            auto issue_s = [&](int t, int j) {
-                const int st = (2 * j) % kRing;
+            constexpr uint32_t kHalf = kM * 8, kTileU = 2 * kHalf;   // 16-byte units of a 64-wide block, of a tile
+            const uint64_t qd = tc::sdesc_sw128(smem_addr(s.q[t][0]), 16, 1024);
+            const uint64_t kd = tc::sdesc_sw128(smem_addr(s.kv[0][0]), 16, 1024);
+            const uint64_t vd = tc::sdesc_sw128(smem_addr(s.kv[0][0]), 2 * kN * 64, 1024);
+            const uint32_t ts = tmem + kColS + t * kN, to = tmem + kColO + t * kD;
+            auto full = [&](int e) { return wait_warp(s, &s.full[e % kRing], (e / kRing) & 1); };
+            auto issue_s = [&](int j) {
+                const uint64_t b = kd + (uint32_t)(2 * j) % kRing * kTileU;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_ss(tmem + kColS + t * kN, tc::sdesc_sw128(smem_addr(s.q[t][kk >> 2]) + (kk & 3) * 32, 16, 1024),
-                               tc::sdesc_sw128(smem_addr(s.kv[st][kk >> 2]) + (kk & 3) * 32, 16, 1024), id_s, kk > 0);
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 2;
+                    tc::mma_ss(ts, qd + o, b + o, id_s, kk > 0);
+                }
                 tc::commit(&s.s_full[t]);
             };
-            auto issue_pv = [&](int t, int j) {
-                const int st = (2 * j + 1) % kRing;
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_ts(tmem + kColO + t * kD, tmem + kColS + t * kN + kk * 8,
-                               tc::sdesc_sw128(smem_addr(s.kv[st][0]) + kk * 2048, 2 * kN * 64, 1024), id_pv,
-                               (j > 0) || (kk > 0));
-            };
-            bool ok = wait(s, &s.q_full, 0) && full(0);
-            if (ok) {
-                tc::fence_after_sync();
-                issue_s(0, 0);
-                issue_s(1, 0);
-                tc::commit(&s.empty[0]);
+            bool ok = wait_warp(s, &s.q_full, 0) && full(0);
+            tc::fence_after_sync();
+            if (ok && tc::elect_one()) {
+                issue_s(0);
+                tc::commit(&s.done[0]);
             }
             for (int j = 0; ok && j < blk.n; ++j) {
                 const bool next = j + 1 < blk.n;
-                ok = full(2 * j + 1) && (!next || full(2 * j + 2));
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    ok = ok && wait(s, &s.p_full[t], j & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    issue_pv(t, j);
-                    if (next) issue_s(t, j + 1);
-                    else tc::commit(&s.o_done[t]);
-                }
+                ok = full(2 * j + 1) && (!next || full(2 * j + 2)) && wait_warp(s, &s.p_full[t], j & 1);
                 if (!ok) break;
-                tc::commit(&s.empty[(2 * j + 1) % kRing]);
-                if (next) tc::commit(&s.empty[(2 * j + 2) % kRing]);
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    const uint64_t b = vd + (uint32_t)(2 * j + 1) % kRing * kTileU;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) tc::mma_ts(to, ts + kk * 8, b + kk * 128, id_pv, (j > 0) || (kk > 0));
+                    if (next) issue_s(j + 1);
+                    else tc::commit(&s.o_done[t]);
+                    tc::commit(&s.done[(j + 1) & 1]);
+                }
+                __syncwarp();
             }
             // every MMA issued here has finished with shared and tensor memory before the CTA frees them
-            tc::commit(&s.drain);
-            mbar_wait(&s.drain, 0);
+            if (tc::elect_one()) tc::commit(&s.drain[t]);
+            __syncwarp();
+            mbar_wait(&s.drain[t], 0);
         }
         __syncwarp();
     } else {
@@ -301,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int k0 = blk.at(j) * kN;
             // every row sees the whole block: no key after the first row's, all in the last row's window or sinks
             const bool whole = k0 + kN - 1 <= ti.p0 && (k0 >= ti.p1 - (a.window - 1) || k0 + kN <= a.n_sink);
-            ok = __all_sync(0xffffffffu, wait(s, &s.s_full[t], j & 1));
+            ok = wait_warp(s, &s.s_full[t], j & 1);
             if (!ok) break;
             tc::fence_after_sync();
             uint32_t x[128];
@@ -320,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // key row r of the V block: an infinity or NaN in it?
                 const int e = 2 * j + 1;
-                ok = __all_sync(0xffffffffu, wait(s, &s.full[e % kRing], (e / kRing) & 1));
+                ok = wait_warp(s, &s.full[e % kRing], (e / kRing) & 1);
                 if (!ok) break;
                 uint32_t bad = 0;
 #pragma unroll
@@ -378,10 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::wait_st();
             tc::fence_before_sync();
-            tc::mbar_arrive(&s.p_full[t]);
+            tc::arrive_warp(&s.p_full[t]);
         }
         // ---------------- epilogue: O / l -> fp16 -> swizzled smem (the Q tile) -> TMA store
-        if (ok) ok = __all_sync(0xffffffffu, wait(s, &s.o_done[t], 0));
+        if (ok) ok = wait_warp(s, &s.o_done[t], 0);
         asm volatile("bar.sync %0, 128;\n" ::"r"(1 + t) : "memory");   // slow[t] is complete
         if (ok) {
             tc::fence_after_sync();
