@@ -67,9 +67,9 @@ struct Smem {
 
 struct Args {
     const uint16_t *q, *k, *v;
-    unsigned *status;   // one word a CTA: 1 = a bounded wait expired, its outputs are not valid
+    unsigned *status;   // one word a query tile: 1 = a bounded wait expired, its outputs are not valid
     int Hq, Hkv, Tq, Tk, window, n_sink;
-    int units, npair, ntile;   // B * Hkv; CTAs and query tiles of a unit
+    int units, ncta, ntile, per;   // B * Hkv; CTAs and query tiles of a unit, tiles of a CTA (1 or 2)
     float scale_log2;
 };
 
@@ -119,49 +119,59 @@ __device__ __forceinline__ Blocks blocks_of(const Args &a, int p0, int p1) {
     return b;
 }
 
-// Row `row` of query head plane bh from scratch, visible keys only (fp32, one thread a row).
-__device__ __noinline__ void slow_row(const Args &a, size_t qrow, size_t kvplane, int p, uint16_t *dst, uint32_t sw) {
-    float o[kD];
-#pragma unroll
-    for (int d = 0; d < kD; ++d) o[d] = 0.f;
-    float m = -INFINITY, l = 0.f;
+// One query row from scratch over its visible keys (fp32, one thread a row): a
+// pass for the maximum and the sum, then 32 channels at a time.
+__device__ __forceinline__ void slow_row(const Args &a, size_t qrow, size_t kvplane, int p, unsigned char *dst, int sw) {
     const uint4 *q = reinterpret_cast<const uint4 *>(a.q + qrow * kD);
     const int lo = max(0, p - (a.window - 1));
-    for (int j = 0; j <= p; ++j) {
-        if (j < lo && j >= a.n_sink) j = lo;
-        const uint4 *kr = reinterpret_cast<const uint4 *>(a.k + (kvplane * a.Tk + j) * kD);
-        const uint4 *vr = reinterpret_cast<const uint4 *>(a.v + (kvplane * a.Tk + j) * kD);
-        float x = 0.f;
-        for (int c = 0; c < 16; ++c) {
-            float qa[8], ka[8];
-            h8_to_f(__ldg(q + c), qa);
-            h8_to_f(__ldg(kr + c), ka);
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int pass = 0; pass < 5; ++pass) {
+        float o[32];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x = fmaf(qa[i], ka[i], x);
+        for (int d = 0; d < 32; ++d) o[d] = 0.f;
+#pragma unroll 1
+        for (int j = 0; j <= p; ++j) {
+            if (j < lo && j >= a.n_sink) j = lo;
+            const uint4 *kr = reinterpret_cast<const uint4 *>(a.k + (kvplane * a.Tk + j) * kD);
+            float x = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+                float qa[8], ka[8];
+                h8_to_f(__ldg(q + c), qa);
+                h8_to_f(__ldg(kr + c), ka);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x = fmaf(qa[i], ka[i], x);
+            }
+            x *= a.scale_log2;
+            if (pass == 0) {
+                const float mn = fmaxf(m, x);
+                l = l * (m == mn ? 1.f : ex2(m - mn)) + (x == -INFINITY ? 0.f : ex2(x - mn));
+                m = mn;
+            } else {
+                const float e = x == -INFINITY ? 0.f : ex2(x - m);
+                const uint4 *vr = reinterpret_cast<const uint4 *>(a.v + (kvplane * a.Tk + j) * kD) + 4 * (pass - 1);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float va[8];
+                    h8_to_f(__ldg(vr + c), va);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[8 * c + i] = fmaf(e, va[i], o[8 * c + i]);
+                }
+            }
         }
-        x *= a.scale_log2;
-        const float mn = fmaxf(m, x);
-        const float al = m == mn ? 1.f : exp2f(m - mn), w = x == -INFINITY ? 0.f : exp2f(x - mn);
-        m = mn;
-        l = fmaf(l, al, w);
+        if (pass == 0) continue;
+        const float inv = 1.f / l;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            float va[8];
-            h8_to_f(__ldg(vr + c), va);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[8 * c + i] = fmaf(o[8 * c + i], al, w * va[i]);
+        for (int c = 0; c < 4; ++c) {   // as the epilogue writes it: 16-byte chunk ch of the row
+            const int ch = 4 * (pass - 1) + c;
+            uint4 u;
+            u.x = pack_half2(o[8 * c] * inv, o[8 * c + 1] * inv);
+            u.y = pack_half2(o[8 * c + 2] * inv, o[8 * c + 3] * inv);
+            u.z = pack_half2(o[8 * c + 4] * inv, o[8 * c + 5] * inv);
+            u.w = pack_half2(o[8 * c + 6] * inv, o[8 * c + 7] * inv);
+            *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kM * 128) + (((ch & 7) ^ sw) << 4)) = u;
         }
-    }
-    const float inv = 1.f / l;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {   // as the epilogue writes it: 16-byte chunk c of the row
-        uint4 w;
-        w.x = pack_half2(o[8 * c] * inv, o[8 * c + 1] * inv);
-        w.y = pack_half2(o[8 * c + 2] * inv, o[8 * c + 3] * inv);
-        w.z = pack_half2(o[8 * c + 4] * inv, o[8 * c + 5] * inv);
-        w.w = pack_half2(o[8 * c + 6] * inv, o[8 * c + 7] * inv);
-        *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(dst) + (c >> 3) * (kM * 128) +
-                                   (((c & 7) ^ sw) << 4)) = w;
     }
 }
 
@@ -174,12 +184,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (broadcast: the compiler then knows that branches on the warp, and descriptors behind them, are uniform)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
-    // the pairs with the longest bands first, all units side by side: their K / V bands overlap in L2
-    const int pair = a.npair - 1 - (int)blockIdx.x / a.units, unit = (int)blockIdx.x % a.units;
+    // the tiles with the longest bands first, all units side by side: their K / V bands overlap in L2
+    const int first = (a.ncta - 1 - (int)blockIdx.x / a.units) * a.per, unit = (int)blockIdx.x % a.units;
     const int b = unit / a.Hkv, kvh = unit - b * a.Hkv;
-    const Tile t0 = tile_of(a, kvh, 2 * pair);
-    const bool two = 2 * pair + 1 < a.ntile;
-    const Tile t1 = two ? tile_of(a, kvh, 2 * pair + 1) : t0;   // an odd last tile is computed twice, stored once
+    const Tile t0 = tile_of(a, kvh, first);
+    const bool two = a.per == 2 && first + 1 < a.ntile;   // else tile 1's warps have nothing to do
+    const Tile t1 = two ? tile_of(a, kvh, first + 1) : t0;
     const Blocks blk = blocks_of(a, min(t0.p0, t1.p0), max(t0.p1, t1.p1));
 
     if (tid == 0) {
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kRing; ++i) mbar_init(&s.full[i], 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s.s_full[t], 1);
-            mbar_init(&s.done[t], 2);     // both issuers
+            mbar_init(&s.done[t], two ? 2 : 1);   // issuers
             mbar_init(&s.drain[t], 1);
             mbar_init(&s.p_full[t], 4);   // warps
             mbar_init(&s.o_done[t], 1);
@@ -209,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::prefetch_map(&map_q);
             tc::prefetch_map(&map_k);
             tc::prefetch_map(&map_v);
-            mbar_arrive_expect_tx(&s.q_full, 4 * kM * 128);
-            for (int t = 0; t < 2; ++t) {
+            mbar_arrive_expect_tx(&s.q_full, (two ? 4 : 2) * kM * 128);
+            for (int t = 0; t < (two ? 2 : 1); ++t) {
                 const Tile &ti = t ? t1 : t0;
                 tc::tma_load_3d(s.q[t][0], &map_q, 0, ti.q0, b * a.Hq + ti.h, &s.q_full);
                 tc::tma_load_3d(s.q[t][1], &map_q, 64, ti.q0, b * a.Hq + ti.h, &s.q_full);
@@ -236,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = issued > kRing ? issued - kRing : 0; e < issued; ++e)
                     mbar_wait(&s.full[e % kRing], (e / kRing) & 1);
             }
-        } else if (warp >= 2) {
+        } else if (warp == 2 || (warp == 3 && two)) {
             // ---------------- MMA issuer of tile t (the warp waits together, one lane issues)
             const int t = warp - 2;
             constexpr uint32_t id_s = tc::idesc_f16(kM, kN, false, false);
@@ -283,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(&s.drain[t], 0);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 8 || two) {
         // ---------------- softmax warps
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
         const int t = warp >= 8;
@@ -387,8 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char *qbytes = reinterpret_cast<unsigned char *>(s.q[t]);
             if (*reinterpret_cast<volatile int *>(&s.slow[t])) {
                 if (ti.q0 + r < a.Tq)
-                    slow_row(a, ((size_t)b * a.Hq + ti.h) * a.Tq + ti.q0 + r, unit, p,
-                             reinterpret_cast<uint16_t *>(qbytes + r * 128), r & 7);
+                    slow_row(a, ((size_t)b * a.Hq + ti.h) * a.Tq + ti.q0 + r, unit, p, qbytes + r * 128, r & 7);
             } else {
                 float la, lb;
                 f2unpack(fadd2(l2a, l2b), la, lb);
@@ -414,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_proxy_async_smem();
         }
         asm volatile("bar.sync %0, 128;\n" ::"r"(1 + t) : "memory");
-        if (ok && (warp & 3) == 0 && lane == 0 && (t == 0 || two)) {
+        if (ok && (warp & 3) == 0 && lane == 0) {
             tc::tma_store_3d(&map_o, s.q[t][0], 0, ti.q0, b * a.Hq + ti.h);
             tc::tma_store_3d(&map_o, s.q[t][1], 64, ti.q0, b * a.Hq + ti.h);
             tc::bulk_commit_group();
@@ -425,21 +434,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     if (warp == 1) tc::tmem_dealloc(tmem, 512);
-    if (tid == 0) a.status[blockIdx.x] = s.abort ? 1u : 0u;
+    if (tid < (two ? 2 : 1)) a.status[unit * a.ntile + first + tid] = s.abort ? 1u : 0u;
 }
 
 std::mutex g_attr_mu;
 bool g_attr[kMaxDevices] = {};
+int g_sms[kMaxDevices] = {};
 
-long long grid_of(int B, int Hq, int Hkv, int Tq) {
-    const long long tiles = ((long long)Tq + kM - 1) / kM * (Hq / Hkv);
-    return (long long)B * Hkv * ((tiles + 1) / 2);
+long long tiles_of(int Hq, int Hkv, int Tq) { return ((long long)Tq + kM - 1) / kM * (Hq / Hkv); }
+
+// Query tiles of a CTA: two share every K / V block they read and hide each
+// other's softmax (8192 tokens, window 4096: 442 us); one while there are SMs for
+// all of them, as a tile alone is done sooner (512 tokens, window 128: CTA of two
+// 16.5 us).
+int tiles_per_cta(int B, int Hq, int Hkv, int Tq, int sms) {
+    return (long long)B * Hkv * tiles_of(Hq, Hkv, Tq) <= sms ? 1 : 2;
 }
 
 }  // namespace
 
-// Workspace: a status word a CTA.
-size_t window_prefill_status_words(int B, int Hq, int Hkv, int Tq) { return (size_t)grid_of(B, Hq, Hkv, Tq); }
+// Workspace: a status word a query tile.
+size_t window_prefill_status_words(int B, int Hq, int Hkv, int Tq) {
+    return (size_t)B * Hkv * (size_t)tiles_of(Hq, Hkv, Tq);
+}
 size_t window_prefill_workspace_bytes(int B, int Hq, int Hkv, int Tq) {
     return (window_prefill_status_words(B, Hq, Hkv, Tq) * 4 + 255) / 256 * 256;
 }
@@ -461,7 +478,6 @@ int window_prefill_launch(const uint16_t *q, const uint16_t *k, const uint16_t *
     a.n_sink = n_sink < Tk ? n_sink : Tk;
     a.units = B * Hkv;
     a.ntile = (Tq + kM - 1) / kM * (Hq / Hkv);
-    a.npair = (a.ntile + 1) / 2;
     a.scale_log2 = sm_scale * kLog2e;
     const size_t smem = sizeof(Smem) + 1024;
     const int dev = current_device();
@@ -472,10 +488,15 @@ int window_prefill_launch(const uint16_t *q, const uint16_t *k, const uint16_t *
             if (cudaFuncSetAttribute(window_fa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
                 cudaSuccess)
                 return check_launch("window_prefill: attribute");
+            int sms = 148;
+            if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) sms = 148;
+            g_sms[dev] = sms;
             g_attr[dev] = true;
         }
+        a.per = tiles_per_cta(B, Hq, Hkv, Tq, g_sms[dev]);
     }
-    window_fa_kernel<<<(unsigned)grid_of(B, Hq, Hkv, Tq), kThreads, smem, stream>>>(mq, mk, mv, mo, a);
+    a.ncta = (a.ntile + a.per - 1) / a.per;
+    window_fa_kernel<<<(unsigned)(a.units * a.ncta), kThreads, smem, stream>>>(mq, mk, mv, mo, a);
     return check_launch("window_prefill");
 }
 

@@ -247,7 +247,7 @@ MINIKV_API int minikv_window_prefill(const uint16_t *q, const uint16_t *k, const
  * workspace finish its work?  As minikv_select_prefill_status: *status = 0, or
  * bit 0 set if a bounded wait expired in some CTA (o is then not valid).
  *   ws, ws_bytes, B, Hq, Hkv, Tq: as passed to that call.
- * Queues device-to-host copies of 4 bytes a CTA on `stream` and synchronizes it.
+ * Queues device-to-host copies of 4 bytes a 128-row query tile on `stream` and synchronizes it.
  * Errors: INVALID_ARG (null, shape, ws smaller than the call's), CUDA.
  */
 MINIKV_API int minikv_window_prefill_status(const void *ws, size_t ws_bytes, int B, int Hq, int Hkv, int Tq,

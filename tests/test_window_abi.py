@@ -54,9 +54,9 @@ def test_window_prefill_refusals(change, code):
 
 
 def test_window_prefill_workspace_and_status_refusals():
-    # a word a CTA: two 128-row tiles each, of 3 heads x 4 tiles a KV head
+    # a word a query tile: 4 tiles of 128 rows of each head, in 256-byte units
     assert mk.workspace_size(mk.OP_WINDOW_PREFILL, 2, 6, 2, 500) == 256
-    assert mk.workspace_size(mk.OP_WINDOW_PREFILL, 4, 32, 8, 4096) == 4 * 8 * 64 * 4
+    assert mk.workspace_size(mk.OP_WINDOW_PREFILL, 4, 32, 8, 4096) == 4 * 32 * 32 * 4
     assert mk.workspace_size(mk.OP_WINDOW_PREFILL, 1, 5, 2, 500) == 0
     L, st = mk.lib(), ctypes.c_uint(0)
     assert L.minikv_window_prefill_status(None, 256, 1, 4, 2, 512, None, ctypes.byref(st)) == mk.ERR_INVALID_ARG
