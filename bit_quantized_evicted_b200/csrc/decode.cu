@@ -281,7 +281,9 @@ struct ArgsDevWin : ArgsDev {
     static constexpr bool kWin = true;
     int window, n_sink;
 };
-// ---- a batch behind a shared prefix: each mode's arguments with the prefix pass's partials
+// ---- a batch behind a shared prefix: each mode's arguments with the prefix pass's partials.  Such a launch follows
+// the prefix pass, which lets it start once all that came before is done: it waits for the pass itself only before
+// it merges the pass's states (at least one unit does: else the pass is not run).
 struct ArgsUniPre : ArgsUni {
     static constexpr bool kPre = true;
     PreTab pre;
@@ -468,6 +470,8 @@ __host__ __device__ __forceinline__ int rvrot(int j) { return ((j >> 1) & 1) + 4
 
 // ---------------------------------------------------------------- partials
 
+__device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
 // The CTA's 16 warp states for the segment's unit (already scaled to the CTA's
 // per-head max and written to sm.wy / wl / wm) are summed into one partial in
 // slot `slot`; the last CTA of the unit to arrive (S_u arrivals) merges the
@@ -533,6 +537,7 @@ __device__ void finish_unit(const A &a, Smem &sm, const Seg &s, const WinSeq &w,
         // the row's states over the shared prefix, from the pass before this kernel
         const PreTab &t = a.pre;
         const int place = t.listed ? t.place[b] : b;
+        if (place >= 0) wait_prior_grid();   // the prefix pass (this kernel did not wait for it at its start)
         if (place >= 0 && h < a.g) {
             const int row = place * a.g + h, pu = (row >> t.lgN) * a.Hkv + kvh, n = row & ((1 << t.lgN) - 1);
             const int c0 = pre_cta(t, pu * t.tpu), c1 = pre_cta(t, pu * t.tpu + t.tpu - 1);
@@ -660,7 +665,6 @@ __device__ __forceinline__ void issue_q(const A &a, uint32_t qb, int u, int lane
 
 // ------------------------------------------------------------------ the CTA
 
-__device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 // kWait: the CTA does its parameter-only set-up, then waits for the previous
@@ -730,7 +734,7 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
         sm.next = xlo + kWarps * (kStages - 1);   // the first kStages-1 items of each warp are fixed
         seg_info(a, c, xlo, xhi, sm.seg);
     }
-    if (kWait) wait_prior_grid();
+    if (kWait && !A::kPre) wait_prior_grid();
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue_next();
     __syncthreads();
@@ -1118,7 +1122,7 @@ template <bool kMass, class A>
 __global__ void __launch_bounds__(kThreads, 1) decode_dev_kernel(const __grid_constant__ A a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     launch_dependents();
-    wait_prior_grid();   // the state table is written by the previous step
+    if (!A::kPre) wait_prior_grid();   // the state table is written by the previous step
     const int tid = threadIdx.x;
     const int B = nseq(a);
     int *nq = dev_arr(a, 0), *rr = dev_arr(a, 1), *rs = dev_arr(a, 2), *ib = dev_arr(a, 3), *clo = dev_arr(a, 4);

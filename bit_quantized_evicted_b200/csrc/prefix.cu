@@ -217,7 +217,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const int g_ = lane >> 2, t_ = lane & 3;
     const int c = blockIdx.x;
 
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.k_full[i], 4);     // warps
@@ -233,7 +232,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         s.abort = 0;
         fence_mbar_init();
     }
+    // The dependents are let go only once everything before this kernel is done: the decode kernel of the step
+    // then starts where SMs are free, with all of its inputs in place, and waits for this grid only where it
+    // merges this grid's states.
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (warp == 1) tc::tmem_alloc(&s.tmem_base, kCols);
     tc::fence_before_sync();
     __syncthreads();
