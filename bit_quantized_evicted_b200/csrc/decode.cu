@@ -1640,7 +1640,7 @@ int launch_mass(const Args &a, const Plan &p, float *mass, long long mass_stride
 
 int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new, int Hq,
                   float sm_scale, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream, float *mass,
-                  int window, int n_sink, const PreTab *pre) {
+                  int window, int n_sink, const PrefixCall *prefix) {
     const Window win = {window, n_sink};
     const int g = Hq / c->Hkv;
     const int ring = c->R + c->G;
@@ -1661,6 +1661,13 @@ int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, con
     if (ws == nullptr || ws_bytes < need)
         return fail(MINIKV_ERR_INVALID_ARG, "decode_attn: workspace of %zu bytes needed, %zu given", need, ws_bytes);
 
+    PreTab tab;
+    const PreTab *pre = nullptr;
+    if (prefix) {   // every check has passed: the prefix pass goes first
+        const int prc = prefix_launch(*prefix, c->B, q, Hq, sm_scale, stream, &tab);
+        if (prc) return prc;
+        if (tab.P) pre = &tab;
+    }
     Args a;
     a.k_codes = c->k_codes; a.v_codes = c->v_codes;
     a.k_scale = c->k_scale; a.k_zero = c->k_zero; a.v_scale = c->v_scale; a.v_zero = c->v_zero;

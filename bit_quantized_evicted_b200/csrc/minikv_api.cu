@@ -37,7 +37,7 @@ int topk_launch(const float *scores, const uint16_t *k, const uint16_t *v, int B
 int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, const uint16_t *v_new, int Hq,
                   float sm_scale, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream,
                   float *mass = nullptr, int window = 0, int n_sink = 0,
-                  const PreTab *pre = nullptr);
+                  const PrefixCall *prefix = nullptr);
 size_t decode_workspace_bytes(int B, int Hkv, int max_tokens);
 size_t decode_mass_workspace_bytes(int B, int Hq, int Hkv, int max_tokens);
 void decode_set_deterministic(int on);
@@ -45,11 +45,8 @@ int window_prefill_launch(const uint16_t *q, const uint16_t *k, const uint16_t *
                           int Tk, int window, int n_sink, float sm_scale, uint16_t *o, void *ws, cudaStream_t stream);
 size_t window_prefill_workspace_bytes(int B, int Hq, int Hkv, int Tq);
 size_t window_prefill_status_words(int B, int Hq, int Hkv, int Tq);
-int prefix_launch(const minikv_cache *p, const int *shared, int B, const uint16_t *q, int Hq, float sm_scale, void *ws,
-                  cudaStream_t stream, PreTab *tab);
 size_t prefix_workspace_bytes(int B, int Hq, int Hkv);
 size_t prefix_status_words();
-size_t decode_call_workspace_bytes(const minikv_cache *c);
 int decode_plan_info(const minikv_cache *c, int *ctas, int *wu, int *first, int n_first);
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -452,18 +449,15 @@ int minikv_decode_attn_prefix(minikv_cache *c, const minikv_cache *prefix, const
         return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: sm_scale must be positive and finite");
     if (!ws) return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: null workspace");
     if (!aligned16(ws)) return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: workspace must be 16-byte aligned");
-    const size_t own = up256(decode_call_workspace_bytes(c)), pre = prefix_workspace_bytes(c->B, Hq, c->Hkv);
-    if (ws_bytes < own + pre)
-        return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: workspace of %zu bytes needed, %zu given", own + pre,
-                    ws_bytes);
     // the prefix pass's part lies at the end, where no call on this workspace keeps arrival counters
-    char *pws = static_cast<char *>(ws) + (ws_bytes - pre) / 256 * 256;
-    PreTab tab;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    rc = prefix_launch(prefix, shared, c->B, q, Hq, sm_scale, pws, s, &tab);
-    if (rc) return rc;
-    return decode_launch(c, q, k_new, v_new, Hq, sm_scale, out, ws, (size_t)(pws - static_cast<char *>(ws)), s, nullptr, 0,
-                         0, tab.P ? &tab : nullptr);
+    const size_t pre = prefix_workspace_bytes(c->B, Hq, c->Hkv);
+    if (ws_bytes < pre)
+        return fail(MINIKV_ERR_INVALID_ARG, "decode_attn_prefix: workspace of more than %zu bytes needed, %zu given", pre,
+                    ws_bytes);
+    const size_t own = (ws_bytes - pre) / 256 * 256;
+    const PrefixCall call = {prefix, shared, static_cast<char *>(ws) + own};
+    return decode_launch(c, q, k_new, v_new, Hq, sm_scale, out, ws, own, static_cast<cudaStream_t>(stream), nullptr, 0, 0,
+                         &call);
 }
 
 int minikv_decode_attn_prefix_status(const void *ws, size_t ws_bytes, int B, int Hq, int Hkv, void *stream,

@@ -798,10 +798,11 @@ size_t prefix_workspace_bytes(int B, int Hq, int Hkv) {
     return prefix_status_bytes() + (kMaxCtas + units) * N * kPreStride * 4;
 }
 
-// Queue the prefix pass: states of the sharing sequences' rows over `p`, and *tab for the merging decode kernel.
-// ws: prefix_workspace_bytes.  shared: host flags a sequence, or NULL (all).  tab->P = 0: nobody attends to anything.
-int prefix_launch(const minikv_cache *p, const int *shared, int B, const uint16_t *q, int Hq, float sm_scale, void *ws,
-                  cudaStream_t stream, PreTab *tab) {
+int prefix_launch(const PrefixCall &call, int B, const uint16_t *q, int Hq, float sm_scale, cudaStream_t stream,
+                  PreTab *tab) {
+    const minikv_cache *p = call.prefix;
+    const int *shared = call.shared;
+    void *ws = call.ws;
     Args a;
     PreTab &t = a.tab;
     const int Hkv = p->Hkv, g = Hq / Hkv;

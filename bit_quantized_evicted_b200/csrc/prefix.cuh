@@ -24,4 +24,18 @@ __host__ __device__ __forceinline__ int pre_cta(const PreTab &t, int x) {
     return (int)((((unsigned long long)x + 1) * (unsigned)t.P - 1) / (unsigned)t.T);
 }
 
+// A step behind a shared prefix, for decode_launch: once its own checks have
+// passed, it queues the prefix pass (prefix_launch) with these before its kernel.
+struct PrefixCall {
+    const minikv_cache *prefix;
+    const int *shared;   // host flags, or NULL: all
+    void *ws;            // prefix_workspace_bytes
+};
+
+// Queue the prefix pass: states of the sharing sequences' rows over p, and *tab
+// for the merging decode kernel (tab->P = 0: nobody attends to anything; nothing
+// but a clearing of the status words is queued).
+int prefix_launch(const PrefixCall &call, int B, const uint16_t *q, int Hq, float sm_scale, cudaStream_t stream,
+                  PreTab *tab);
+
 }  // namespace minikv
