@@ -72,7 +72,7 @@ struct Smem {
     float m[N], alpha[2][N], l[N], pz[N];
     float wmax[4][N];
     int resc[2][2];                     // [stage][half]: the tile moved the references (alpha holds the factors)
-    uint64_t k_full[2], k_empty[2], kz_full[2], t_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain[2];
+    uint64_t k_full[2], k_empty[2], kz_full[2], t_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain[2];   // in this order
     uint32_t tmem_base;
     int abort;
 };
@@ -217,20 +217,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const int g_ = lane >> 2, t_ = lane & 3;
     const int c = blockIdx.x;
 
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.k_full[i], 4);     // warps
-            mbar_init(&s.k_empty[i], 1 + kTW);   // S has read K', the T warps the scales and zeros
-            mbar_init(&s.kz_full[i], 4);
-            mbar_init(&s.t_full[i], kTW);
-            mbar_init(&s.v_full[i], 4);
-            mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.drain[i], 1);
-            mbar_init(&s.p_full[i], 8);
-            mbar_init(&s.o_done[i], 1 + kSW);    // O'^T has the tile; the sum warps have its sums
-        }
-        s.abort = 0;
+    if (warp == 0) {
+        // arrivals a phase: k_full 4 (warps), k_empty S and the T warps, kz_full 4, t_full the T warps, v_full 4,
+        // s_full 1, p_full 8 (warps), o_done O'^T and the sum warps, drain 1
+        constexpr unsigned long long kCounts = 4ull | (1ull + kTW) << 4 | 4ull << 8 | (unsigned long long)kTW << 12 |
+                                               4ull << 16 | 1ull << 20 | 8ull << 24 | (1ull + kSW) << 28 | 1ull << 32;
+        if (lane < 18) mbar_init(&s.k_full[0] + lane, (uint32_t)(kCounts >> (4 * (lane >> 1))) & 15u);
         fence_mbar_init();
+        if (lane == 0) s.abort = 0;
     }
     // The dependents are let go only once everything before this kernel is done: the decode kernel of the step
     // then starts where SMs are free, with all of its inputs in place, and waits for this grid only where it

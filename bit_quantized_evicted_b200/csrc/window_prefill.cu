@@ -56,10 +56,10 @@ constexpr float kNone = -1e30f;             // reference max of a row that has s
 struct Smem {
     uint16_t q[2][2][kM * 64];       // [tile][64-wide d block], 128-byte swizzle
     uint16_t kv[kRing][2][kN * 64];
+    // mbarriers, initialised by kBars lanes at once
     uint64_t q_full, full[kRing];
-    uint64_t done[2];                // step 0, S(0), and j + 1, P V(j) and S(j + 1), of both tiles have read their blocks
-    uint64_t s_full[2], p_full[2], o_done[2];
-    uint64_t drain[2];
+    uint64_t done[2];                // step 0, S(0), and j + 1, P V(j) and S(j + 1), of every tile have read their blocks
+    uint64_t p_full[2], s_full[2], o_done[2], drain[2];
     uint32_t tmem_base;
     int abort;
     int slow[2];                     // tile t met an infinity or NaN in a partly visible V block
@@ -192,21 +192,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Tile t1 = two ? tile_of(a, kvh, first + 1) : t0;
     const Blocks blk = blocks_of(a, min(t0.p0, t1.p0), max(t0.p1, t1.p1));
 
-    if (tid == 0) {
-        mbar_init(&s.q_full, 1);
-        for (int i = 0; i < kRing; ++i) mbar_init(&s.full[i], 1);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&s.s_full[t], 1);
-            mbar_init(&s.done[t], two ? 2 : 1);   // issuers
-            mbar_init(&s.drain[t], 1);
-            mbar_init(&s.p_full[t], 4);   // warps
-            mbar_init(&s.o_done[t], 1);
-            s.slow[t] = 0;
-        }
-        s.abort = 0;
+    constexpr int kBars = 1 + kRing + 10;
+    if (warp == 0) {
+        const int i = lane - (1 + kRing);
+        if (lane < kBars) mbar_init(&s.q_full + lane, i < 0 || i > 3 ? 1 : i > 1 ? 4 : two ? 2 : 1);   // done: issuers; p_full: warps
         fence_mbar_init();
+        if (lane < 2) s.slow[lane] = 0;
+        if (lane == 0) s.abort = 0;
     }
     if (warp == 1) tc::tmem_alloc(&s.tmem_base, 512);
+    // A programmatic dependent of the work before it: the set-up above may run under that work's tail, every
+    // access to global memory comes after this wait.
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -427,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tma_store_3d(&map_o, s.q[t][0], 0, ti.q0, b * a.Hq + ti.h);
             tc::tma_store_3d(&map_o, s.q[t][1], 64, ti.q0, b * a.Hq + ti.h);
             tc::bulk_commit_group();
-            tc::bulk_wait_all();
+            tc::bulk_wait_read();
         }
     }
     tc::fence_before_sync();
@@ -496,7 +494,17 @@ int window_prefill_launch(const uint16_t *q, const uint16_t *k, const uint16_t *
         a.per = tiles_per_cta(B, Hq, Hkv, Tq, g_sms[dev]);
     }
     a.ncta = (a.ntile + a.per - 1) / a.per;
-    window_fa_kernel<<<(unsigned)(a.units * a.ncta), kThreads, smem, stream>>>(mq, mk, mv, mo, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.units * a.ncta));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, window_fa_kernel, mq, mk, mv, mo, a);
     return check_launch("window_prefill");
 }
 
