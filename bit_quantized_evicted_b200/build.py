@@ -22,6 +22,7 @@ SOURCES = ["minikv_api.cu", "pack.cu", "prefill.cu", "window_prefill.cu", "topk.
            "decode_static.cu", "prefix.cu"]
 # sources with bounded waits: compiled once more for the wait-probe library
 PROBE_SOURCES = ["prefill.cu", "window_prefill.cu", "prefix.cu"]
+PROBE_FLAGS = ["-DMINIKV_WAIT_LIMIT=1", "-DMINIKV_ROLE_WAIT_LIMIT=1"]
 HEADERS = ["common.cuh", "tc.cuh", "prefix.cuh"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = [
@@ -58,7 +59,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
         o = os.path.join(BUILD, src.replace(".cu", "_waitprobe.o"))
         probe_objs[SOURCES.index(src)] = o
         if force or _stale(o, [s, *hdrs]):
-            jobs.append([NVCC, *FLAGS, "-DMINIKV_WAIT_LIMIT=1", "-DMINIKV_ROLE_WAIT_LIMIT=1", "-c", s, "-o", o])
+            jobs.append([NVCC, *FLAGS, *PROBE_FLAGS, "-c", s, "-o", o])
     with cf.ThreadPoolExecutor(max_workers=min(8, max(1, len(jobs)))) as ex:
         for res in ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs):
             if res.returncode != 0:

@@ -196,6 +196,11 @@ constexpr uint32_t kSuspendNs = 16384;
 // up to n polls
 __device__ __forceinline__ uint32_t poll(uint64_t *bar, uint32_t parity, uint32_t n) {
     uint32_t done;
+#if MINIKV_ROLE_WAIT_LIMIT == 1   // the build whose waits give up at once: try_wait would suspend first, whatever its hint
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return done;
+#endif
     asm volatile(
         "{\n .reg .pred p, q;\n .reg .b32 n;\n mov.b32 n, %4;\n"
         "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n @p bra OVER;\n"
