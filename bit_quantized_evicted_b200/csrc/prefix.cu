@@ -55,6 +55,7 @@ namespace {
 
 constexpr int kTile = 128;      // tokens of a tile
 constexpr int kThreads = 768;
+constexpr int kMaxCtas = 148;   // one a SM
 constexpr float kLazy = 8.f;
 // words of a quarter's scales and zeros: the eight columns that T reads side by side lie in distinct banks
 constexpr int kKszZero = 68, kKszStride = 136;
@@ -747,14 +748,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     }
     __syncthreads();
     if (warp == 1) tc::tmem_dealloc(tmem, kCols);
-    if (tid == 0) a.status[c] = s.abort ? 1u : 0u;
+    // (words of CTAs that this call does not have: zero)
+    if (tid < kMaxCtas && tid % a.tab.P == c) a.status[tid] = tid == c && s.abort ? 1u : 0u;
 }
 
 std::mutex g_mu;
 bool g_attr[kMaxDevices] = {};
 int g_sms[kMaxDevices] = {};
-
-constexpr int kMaxCtas = 148;   // one a SM
 
 int row_tile(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
