@@ -306,6 +306,7 @@ int minikv_window_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *
     const size_t need = window_prefill_workspace_bytes(B, Hq, Hkv, Tq);
     if (ws_bytes < need)
         return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: workspace of %zu bytes needed, %zu given", need, ws_bytes);
+    if (o == k || o == v) return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: o lies over k or v");
     return window_prefill_launch(q, k, v, B, Hq, Hkv, Tq, Tk, window, n_sink, sm_scale, o, ws,
                                  static_cast<cudaStream_t>(stream));
 }

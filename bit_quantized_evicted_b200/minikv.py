@@ -8,6 +8,7 @@ tensor of the right dtype, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -97,7 +98,7 @@ def _check(rc: int) -> None:
 def _dev(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise TypeError(f"{name} must be contiguous")
@@ -108,11 +109,46 @@ def _dev(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_cuda_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream, device) -> int:
     if stream is None and _raw_stream is not None and device.index is not None:
         return _raw_stream(device.index)
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return s.cuda_stream
+
+
+def _elsewhere(stream, t: torch.Tensor, *others: torch.Tensor):
+    """None where a call on `t` and `others` may run as things are.  Else what to
+    run it under: their device made current (the library launches on the current
+    one), and `stream`, so that what the call allocates belongs to the stream it
+    runs on."""
+    d = t.get_device()
+    for x in others:
+        if x.get_device() != d:
+            raise ValueError(f"tensors on {t.device} and {x.device}")
+    if stream is None and (d < 0 or d == _cuda_device()):
+        return None
+    under = contextlib.ExitStack()
+    if d >= 0:
+        under.enter_context(torch.cuda.device(d))
+    if stream is not None:
+        under.enter_context(torch.cuda.stream(stream))
+    return under
+
+
+def _check_step(cache, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, out):
+    """Shape [B, Hq, D] of a decode step on `cache`, the other tensors' checked against it."""
+    c, shape = cache.c, q.shape
+    B, Hq, D = shape
+    if B != c.B or D != c.D:
+        raise ValueError(f"q {tuple(shape)} does not match a cache of B={c.B}, D={c.D}")
+    if k_new.shape != (B, c.Hkv, D) or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new {tuple(k_new.shape)}, v_new {tuple(v_new.shape)}: both must be {(B, c.Hkv, D)}")
+    if out is not None and out.shape != shape:
+        raise ValueError(f"out {tuple(out.shape)} does not match q {tuple(shape)}")
+    return shape
 
 
 def workspace_size(op: int, B: int, Hq: int, Hkv: int, T: int, D: int = 128, W: int = 0) -> int:
@@ -314,17 +350,21 @@ def window_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: in
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not match")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(D)
+    if o is not None and o.shape != q.shape:
+        raise ValueError(f"o {tuple(o.shape)} does not match q {tuple(q.shape)}")
+    under = _elsewhere(stream, q, k, v)
+    if under is not None:
+        with under:
+            return window_prefill(q, k, v, window, n_sink, sm_scale, o, ws, None, library)
     if o is None:
         o = torch.empty_like(q)
-    elif o.shape != q.shape:
-        raise ValueError(f"o {tuple(o.shape)} does not match q {tuple(q.shape)}")
     if ws is None:
         ws = torch.empty(max(workspace_size(OP_WINDOW_PREFILL, B, Hq, Hkv, Tq, D), 256), dtype=torch.uint8,
                          device=q.device)
     _check((library or lib()).minikv_window_prefill(
         _dev(q, torch.float16, "q"), _dev(k, torch.float16, "k"), _dev(v, torch.float16, "v"), B, Hq, Hkv, Tq, Tk, D,
         int(window), int(n_sink), float(sm_scale), _dev(o, torch.float16, "o"), _dev(ws, torch.uint8, "ws"), ws.numel(),
-        _stream(stream, q.device)))
+        _stream(None, q.device)))
     return o
 
 
@@ -418,17 +458,21 @@ def decode_attn_window(cache: MiniKVCache, q: torch.Tensor, k_new: torch.Tensor,
                        ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """decode_attn that attends to the newest `window` tokens (the new one
     included) and the first `n_sink` of each sequence, in order of arrival."""
-    B, Hq, D = q.shape
+    if ws is None:
+        ws = cache.ws
+    under = _elsewhere(stream, q, k_new, v_new, ws)
+    if under is not None:
+        with under:
+            return decode_attn_window(cache, q, k_new, v_new, window, n_sink, sm_scale, out, ws)
+    B, Hq, D = _check_step(cache, q, k_new, v_new, out)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(D)
     if out is None:
         out = torch.empty_like(q)
-    if ws is None:
-        ws = cache.ws
     _check(lib().minikv_decode_attn_window(
         ctypes.byref(cache.c), _dev(q, torch.float16, "q"), _dev(k_new, torch.float16, "k_new"),
         _dev(v_new, torch.float16, "v_new"), Hq, int(window), int(n_sink), float(sm_scale),
-        _dev(out, torch.float16, "out"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream, q.device)))
+        _dev(out, torch.float16, "out"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(None, q.device)))
     return out
 
 
@@ -443,8 +487,13 @@ def decode_attn_prefix(cache: MiniKVCache, prefix: MiniKVCache, q: torch.Tensor,
                        library=None) -> torch.Tensor:
     """decode_attn of a batch whose sequences (all, or those flagged in `shared`)
     also attend to every token of `prefix`, a cache of one sequence.  The default
-    workspace is made once per cache, zero-filled, and kept on it."""
-    B, Hq, D = q.shape
+    workspace is made once per cache, zero-filled, and kept on it (not while a
+    graph is captured: the graph would own it)."""
+    under = _elsewhere(stream, q, k_new, v_new)
+    if under is not None:
+        with under:
+            return decode_attn_prefix(cache, prefix, q, k_new, v_new, shared, sm_scale, out, ws, None, library)
+    B, Hq, D = _check_step(cache, q, k_new, v_new, out)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(D)
     if out is None:
@@ -452,17 +501,20 @@ def decode_attn_prefix(cache: MiniKVCache, prefix: MiniKVCache, q: torch.Tensor,
     if shared is not None:
         if len(shared) != B:
             raise ValueError(f"{len(shared)} flags for {B} sequences")
-        if not isinstance(shared, ctypes.Array):
+        if not (isinstance(shared, ctypes.Array) and shared._type_ is _I):
             shared = shared_rows(shared)
     if ws is None:
         need = workspace_size(OP_DECODE_ATTN_PREFIX, B, Hq, cache.Hkv, cache.cap + cache.R + cache.G, D)
         if getattr(cache, "ws_prefix", None) is None or cache.ws_prefix.numel() < need:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("decode_attn_prefix: the first call on a cache makes its workspace, which a captured "
+                                   "call cannot; pass ws or make a call before the capture")
             cache.ws_prefix = torch.zeros(need, dtype=torch.uint8, device=cache.device)
         ws = cache.ws_prefix
     _check((library or lib()).minikv_decode_attn_prefix(
         ctypes.byref(cache.c), ctypes.byref(prefix.c), shared, _dev(q, torch.float16, "q"),
         _dev(k_new, torch.float16, "k_new"), _dev(v_new, torch.float16, "v_new"), Hq, float(sm_scale),
-        _dev(out, torch.float16, "out"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream, q.device)))
+        _dev(out, torch.float16, "out"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(None, q.device)))
     return out
 
 

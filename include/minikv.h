@@ -223,7 +223,8 @@ MINIKV_API int minikv_select_prefill_status(const void *ws, size_t ws_bytes, int
  *   q [B, Hq, Tq, D], k, v [B, Hkv, Tk, D] fp16, 1 <= Tq <= Tk: the queries are
  *   the last Tq of Tk positions (Tq = Tk: a whole prompt; Tq < Tk: a chunk
  *   against everything before it).
- *   o [B, Hq, Tq, D] fp16: with p = Tk - Tq + i the position of query row i,
+ *   o [B, Hq, Tq, D] fp16, q itself or clear of q, k and v: with p = Tk - Tq + i
+ *       the position of query row i,
  *       o_i = sum_j softmax_j(sm_scale * q_i.k_j) v_j over the keys j <= p with
  *       p - j < window or j < n_sink.
  *   window >= 1, n_sink >= 0; window >= Tk is causal attention over all keys.
@@ -234,8 +235,8 @@ MINIKV_API int minikv_select_prefill_status(const void *ws, size_t ws_bytes, int
  *   ws: device scratch of minikv_workspace_size(MINIKV_OP_WINDOW_PREFILL, B, Hq,
  *       Hkv, Tq, D, 0) bytes, no initial contents required; it holds the call's
  *       status words (minikv_window_prefill_status).
- * Errors: INVALID_ARG (null, misaligned, Tq > Tk, Hq % Hkv, window < 1,
- * n_sink < 0, sm_scale <= 0, ws too small), UNSUPPORTED (D != 128, B*Hq above
+ * Errors: INVALID_ARG (null, misaligned, o at k or v, Tq > Tk, Hq % Hkv, window
+ * < 1, n_sink < 0, sm_scale <= 0, ws too small), UNSUPPORTED (D != 128, B*Hq above
  * 65535, Tk above 2^30), CUDA (tensor-map encoding or launch failed).
  */
 MINIKV_API int minikv_window_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *v, int B, int Hq, int Hkv,
