@@ -31,10 +31,10 @@
 // Hidden keys are -inf before the max, and the reference starts at a finite
 // -1e30, so a block without a visible key for a row leaves that row as it was.
 //
-// A hidden key's value row meets P = 0 in the tensor cores, and 0 * inf is not
-// 0: in the blocks that are only partly visible the softmax threads look at the
-// V tile, and if it holds an infinity or NaN the tile's rows are computed again
-// by slow_row (CUDA cores, visible keys only).
+// A hidden key's value row meets P = 0 in the tensor cores, and 0 times an
+// infinity or NaN is NaN, which stays in O: a row whose weights are finite and
+// whose output is not is computed again by slow_row (CUDA cores, visible keys
+// only).
 #include <math.h>
 
 #include <mutex>
@@ -62,7 +62,6 @@ struct Smem {
     uint64_t p_full[2], s_full[2], o_done[2], drain[2];
     uint32_t tmem_base;
     int abort;
-    int slow[2];                     // tile t met an infinity or NaN in a partly visible V block
 };
 
 struct Args {
@@ -197,7 +196,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = lane - (1 + kRing);
         if (lane < kBars) mbar_init(&s.q_full + lane, i < 0 || i > 3 ? 1 : i > 1 ? 4 : two ? 2 : 1);   // done: issuers; p_full: warps
         fence_mbar_init();
-        if (lane < 2) s.slow[lane] = 0;
         if (lane == 0) s.abort = 0;
     }
     if (warp == 1) tc::tmem_alloc(&s.tmem_base, 512);
@@ -325,21 +323,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i)
                         if (!(seen >> i & 1)) x[32 * c + i] = __float_as_uint(-INFINITY);
                 }
-                // key row r of the V block: an infinity or NaN in it?
-                const int e = 2 * j + 1;
-                ok = wait_warp(s, &s.full[e % kRing], (e / kRing) & 1);
-                if (!ok) break;
-                uint32_t bad = 0;
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(&s.kv[e % kRing][c >> 3][r * 64 + 8 * ((c ^ r) & 7)]);
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // exponent 31 carries into bit 15 of each half
-                        bad |= (u[i] & 0x7C007C00u) + 0x04000400u;
-                    }
-                }
-                if (bad & 0x80008000u) *reinterpret_cast<volatile int *>(&s.slow[t]) = 1;
             }
             float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
@@ -389,35 +372,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // ---------------- epilogue: O / l -> fp16 -> swizzled smem (the Q tile) -> TMA store
         if (ok) ok = wait_warp(s, &s.o_done[t], 0);
-        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + t) : "memory");   // slow[t] is complete
         if (ok) {
             tc::fence_after_sync();
             unsigned char *qbytes = reinterpret_cast<unsigned char *>(s.q[t]);
-            if (*reinterpret_cast<volatile int *>(&s.slow[t])) {
-                if (ti.q0 + r < a.Tq)
-                    slow_row(a, ((size_t)b * a.Hq + ti.h) * a.Tq + ti.q0 + r, unit, p, qbytes + r * 128, r & 7);
-            } else {
-                float la, lb;
-                f2unpack(fadd2(l2a, l2b), la, lb);
-                const float inv = 1.f / (la + lb);
+            float la, lb;
+            f2unpack(fadd2(l2a, l2b), la, lb);
+            const float l = la + lb, inv = 1.f / l;
+            uint32_t bad = 0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tc::tmem_ld32(to + 32 * c, o);
-                    tc::wait_ld();
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tc::tmem_ld32(to + 32 * c, o);
+                tc::wait_ld();
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {   // 16-byte chunk: d = 32c + 8u .. +7
-                        const int d = 32 * c + 8 * u;
-                        const int kb = d >> 6, ch = (d & 63) >> 3;
-                        uint4 w;
-                        w.x = pack_half2(__uint_as_float(o[8 * u + 0]) * inv, __uint_as_float(o[8 * u + 1]) * inv);
-                        w.y = pack_half2(__uint_as_float(o[8 * u + 2]) * inv, __uint_as_float(o[8 * u + 3]) * inv);
-                        w.z = pack_half2(__uint_as_float(o[8 * u + 4]) * inv, __uint_as_float(o[8 * u + 5]) * inv);
-                        w.w = pack_half2(__uint_as_float(o[8 * u + 6]) * inv, __uint_as_float(o[8 * u + 7]) * inv);
-                        *reinterpret_cast<uint4 *>(qbytes + kb * (kM * 128) + r * 128 + ((ch ^ (r & 7)) << 4)) = w;
+                for (int u = 0; u < 4; ++u) {   // 16-byte chunk: d = 32c + 8u .. +7
+                    const int d = 32 * c + 8 * u;
+                    const int kb = d >> 6, ch = (d & 63) >> 3;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {   // exponent 31 carries into bit 15 of each half
+                        w[i] = pack_half2(__uint_as_float(o[8 * u + 2 * i]) * inv, __uint_as_float(o[8 * u + 2 * i + 1]) * inv);
+                        bad |= (w[i] & 0x7C007C00u) + 0x04000400u;
                     }
+                    *reinterpret_cast<uint4 *>(qbytes + kb * (kM * 128) + r * 128 + ((ch ^ (r & 7)) << 4)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
+            // (weights that are NaN themselves, or none at all, give NaN whatever the values are)
+            if ((bad & 0x80008000u) && l > 0.f && l < INFINITY && ti.q0 + r < a.Tq)
+                slow_row(a, ((size_t)b * a.Hq + ti.h) * a.Tq + ti.q0 + r, unit, p, qbytes + r * 128, r & 7);
             tc::fence_proxy_async_smem();
         }
         asm volatile("bar.sync %0, 128;\n" ::"r"(1 + t) : "memory");

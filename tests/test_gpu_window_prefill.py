@@ -163,3 +163,20 @@ def test_expired_waits_are_reported():
     o = mk.window_prefill(q, k, v, 300, 4, ws=ws)
     assert mk.window_prefill_status(ws, 1, 4, 2, 1000) == 0
     _check(o, q, k, v, 300, 4, torch.arange(0, 1000, 37, device=DEV))
+
+
+def test_nan_stays_with_the_rows_that_see_it():
+    """A NaN query row spoils itself alone; a value that is not finite the rows that see its key, in its channel."""
+    T, window, n_sink, row, key, ch = 700, 150, 3, 300, 400, 17
+    q, k, v = _qkv(1, 4, 2, T, T, seed=901)
+    clean, q0, v0 = mk.window_prefill(q, k, v, window, n_sink), q.clone(), v.clone()
+    q[0, 1, row] = float("nan")
+    v[0, 1, key, ch] = float("inf")
+    o = mk.window_prefill(q, k, v, window, n_sink)
+    assert torch.isnan(o[0, 1, row]).all()
+    o[0, 1, row] = clean[0, 1, row]
+    assert torch.equal(o[0, :2], clean[0, :2])
+    seen = _seen(T, T, window, n_sink)[:, key]
+    assert not torch.isfinite(o[0, 2:, seen, ch]).any()
+    o[0, 2:, seen, ch] = clean[0, 2:, seen, ch]
+    _check(o, q0, k, v0, window, n_sink)   # (rows that share a block with the value are computed again)
