@@ -68,12 +68,12 @@ struct Smem {
     uint16_t q[2][N * 64];              // [64-channel block][row][64]
     uint32_t ksz[2][4][kKszStride];     // [stage][quarter]: scale pairs [64], zero pairs [64] of its key group
     uint32_t vz[2][2][kTile / 2];       // [stage][hi, lo]: fp16 z + o s of the value tokens
-    float tz[2][4][N];                  // [stage][quarter][row]: T in log2 units
+    float tz[4][4][N];                  // [tile & 3][quarter][row]: T in log2 units
     float bias[8][N / 2];               // a softmax warp's T - reference of the tile in hand
     float m[N], alpha[2][N], l[N], pz[N];
     float wmax[4][N];
     int resc[2][2];                     // [stage][half]: the tile moved the references (alpha holds the factors)
-    uint64_t k_full[2], k_empty[2], kz_full[2], t_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain[2];   // in this order
+    uint64_t k_full[2], k_empty[2], kz_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain[2];   // in this order
     uint32_t tmem_base;
     int abort;
 };
@@ -219,11 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const int c = blockIdx.x;
 
     if (warp == 0) {
-        // arrivals a phase: k_full 4 (warps), k_empty S and the T warps, kz_full 4, t_full the T warps, v_full 4,
-        // s_full 1, p_full 8 (warps), o_done O'^T and the sum warps, drain 1
-        constexpr unsigned long long kCounts = 4ull | (1ull + kTW) << 4 | 4ull << 8 | (unsigned long long)kTW << 12 |
-                                               4ull << 16 | 1ull << 20 | 8ull << 24 | (1ull + kSW) << 28 | 1ull << 32;
-        if (lane < 18) mbar_init(&s.k_full[0] + lane, (uint32_t)(kCounts >> (4 * (lane >> 1))) & 15u);
+        // arrivals a phase: k_full 4 (warps), k_empty S and the T warps, kz_full 4, v_full 4,
+        // s_full the MMA and the T warps, p_full 8 (warps), o_done O'^T and the sum warps, drain 1
+        constexpr unsigned long long kCounts = 4ull | (1ull + kTW) << 4 | 4ull << 8 |
+                                               4ull << 12 | (1ull + kTW) << 16 | 8ull << 20 | (1ull + kSW) << 24 | 1ull << 28;
+        if (lane < 16) mbar_init(&s.k_full[0] + lane, (uint32_t)(kCounts >> (4 * (lane >> 1))) & 15u);
         fence_mbar_init();
         if (lane == 0) s.abort = 0;
     }
@@ -279,11 +279,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 for (int i = 0; i < sg.n; ++i) {
                     const int k = it + i, st = k & 1;
                     const uint32_t keep = sg.x0 + i < a.nt_packed ? 0xffffffffu : 0u;   // fp16 tokens have no T
-                    // tz of two tiles ago has been read
-                    if (!wait_warp(s, &s.kz_full[st], ph(k)) || (k >= 2 && !wait_warp(s, &s.p_full[st], ph_prev(k)))) break;
+                    // (tz of four tiles ago has been read: K of this tile came after S of two ago, which came after P of four)
+                    if (!wait_warp(s, &s.kz_full[st], ph(k))) break;
                     // column g_: z of quarter g_, then s of quarter g_ - 4
                     const uint32_t *col = s.ksz[st][g_ & 3] + (g_ < 4 ? kKszZero : 0) + t_;
-                    float *tz = &s.tz[st][2 * (t_ & 1)][(warp >> 1) * MT * 16 + g_];
+                    float *tz = &s.tz[k & 3][2 * (t_ & 1)][(warp >> 1) * MT * 16 + g_];
 #pragma unroll 1
                     for (int m0 = 0; m0 < MT; m0 += MB) {
                         float d[MB][2][4];
@@ -315,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                                 if (t_ < 2) tz[(e & 1) * N + 16 * (m0 + m) + 8 * (e >> 1)] = v * sc;
                             }
                     }
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc::mbar_arrive(&s.t_full[st]);
-                        tc::mbar_arrive(&s.k_empty[st]);
-                    }
+                    tc::arrive_warp(&s.k_empty[st]);
+                    // P and the factors of two tiles ago have been read (waited for here: the softmax warps then wait
+                    // once a tile, and a wait that is over takes 250 cycles)
+                    if (k >= 2 && !wait_warp(s, &s.o_done[st], ph_prev(k))) break;
+                    tc::arrive_warp(&s.s_full[st]);
                 }
             } else if (warp == 1) {
                 // ---------------- S'^T = K' Q^T (the warp waits together, one lane issues)
@@ -533,10 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 const int k = it + i, st = k & 1, xt = sg.x0 + i;
                 const bool live = xt < a.nt_packed ? xt * kTile + r < a.n_packed
                                                    : (xt - a.nt_packed) * kTile + r < a.n_res;
-                // T of the tile; P, alpha and the flag of two tiles ago have been read
-                ok = ok && wait_warp(s, &s.t_full[st], ph(k)) && (k < 2 || wait_warp(s, &s.o_done[st], ph_prev(k)));
-                for (int j = lane; j < C; j += 32) bias[j] = s.tz[st][quad][n0 + j] - s.m[n0 + j];
-                __syncwarp();
+                // S and T of the tile; P, alpha and the flag of two tiles ago have been read
                 ok = ok && wait_warp(s, &s.s_full[st], ph(k));
                 tc::fence_after_sync();
                 const uint32_t ts = tmem + lanes + kColS + st * N + n0;
@@ -544,8 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 // the tile's log2 scores relative to the references; a second time if these move
                 // (C = 64: 32 at a time and read twice, so that the loop stays in the instruction cache)
                 float x[CH];
-                auto load = [&](int j0) {
-                    tc::tmem_ld<CH>(ts + j0, *reinterpret_cast<uint32_t(*)[CH]>(&x[0]));
+                auto fetch = [&](int j0) { tc::tmem_ld<CH>(ts + j0, *reinterpret_cast<uint32_t(*)[CH]>(&x[0])); };
+                auto arrived = [&](int j0) {
                     tc::wait_ld();
 #pragma unroll
                     for (int j = 0; j < CH; j += 4) {
@@ -556,10 +553,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 };
                 bool moved = false, aborted = false;
                 for (;;) {
+                    fetch(0);
+                    for (int j = lane; j < C; j += 32) bias[j] = s.tz[k & 3][quad][n0 + j] - s.m[n0 + j];
+                    __syncwarp();
                     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
                     for (int j0 = 0; j0 < C; j0 += CH) {
-                        load(j0);
+                        if (j0) fetch(j0);
+                        arrived(j0);
 #pragma unroll
                         for (int j = 0; j < CH; j += 4) {
                             mx0 = max3(mx0, x[j], x[j + 1]);
@@ -597,8 +598,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                         s.alpha[st][n] = i > 0 ? ex2(-up) : 1.f;
                     }
                     sync_half(bar);
-                    for (int j = lane; j < C; j += 32) bias[j] = s.tz[st][quad][n0 + j] - s.m[n0 + j];
-                    __syncwarp();
                     if (i > 0) {
                         ok = wait_warp(s, &s.o_done[(k - 1) & 1], ph(k - 1));
                         tc::fence_after_sync();
@@ -625,7 +624,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 unsigned char *row = reinterpret_cast<unsigned char *>(s.p[st][n0 >> 6]) + r * 128;
 #pragma unroll 1
                 for (int j0 = 0; j0 < C; j0 += CH) {
-                    if (C > CH) load(j0);
+                    if (C > CH) {
+                        fetch(j0);
+                        arrived(j0);
+                    }
 #pragma unroll
                     for (int j = 0; j < CH; j += 8) {
                         uint32_t w[4];
