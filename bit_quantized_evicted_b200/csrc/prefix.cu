@@ -54,7 +54,7 @@ namespace minikv {
 namespace {
 
 constexpr int kTile = 128;      // tokens of a tile
-constexpr int kThreads = 768;
+constexpr int kThreads = 1024;
 constexpr int kMaxCtas = 148;   // one a SM
 constexpr float kLazy = 8.f;
 // words of a quarter's scales and zeros: the eight columns that T reads side by side lie in distinct banks
@@ -69,10 +69,10 @@ struct Smem {
     uint32_t ksz[2][4][kKszStride];     // [stage][quarter]: scale pairs [64], zero pairs [64] of its key group
     uint32_t vz[2][2][kTile / 2];       // [stage][hi, lo]: fp16 z + o s of the value tokens
     float tz[4][4][N];                  // [tile & 3][quarter][row]: T in log2 units
-    float bias[8][N / 2];               // a softmax warp's T - reference of the tile in hand
+    float bias[16][N / 2];               // a softmax warp's T - reference of the tile in hand
     float m[N], alpha[2][N], l[N], pz[N];
     float wmax[4][N];
-    int resc[2][2];                     // [stage][half]: the tile moved the references (alpha holds the factors)
+    int resc[2][4];                     // [stage][part]: the tile moved the references (alpha holds the factors)
     uint64_t k_full[2], k_empty[2], kz_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain[2];   // in this order
     uint32_t tmem_base;
     int abort;
@@ -167,13 +167,24 @@ __device__ __forceinline__ uint32_t or_over(int bar, uint32_t x) {   // over the
 }
 __device__ __forceinline__ void sync_all() { asm volatile("barrier.cta.sync 0, %0;\n" ::"n"(kThreads) : "memory"); }
 __device__ __forceinline__ void sync_half(int bar) { asm volatile("barrier.cta.sync %0, 128;\n" ::"r"(bar) : "memory"); }
-// largest of a warp's values (through the order of the bits as integers)
-__device__ __forceinline__ float warp_max(float x) {
-    int i = __float_as_int(x);
-    i ^= (i >> 31) & 0x7fffffff;
-    i = __reduce_max_sync(0xffffffffu, i);
-    i ^= (i >> 31) & 0x7fffffff;
-    return __int_as_float(i);
+// Column maxima of a warp's [32 lanes x C]: x[0] of lane l becomes that of column
+// l / (32 / C).  Lanes a bit apart halve their columns between them, step by step.
+template <int C, int BIT>
+__device__ __forceinline__ void col_max(float *x, int lane) {
+    if constexpr (BIT > 0) {
+        if constexpr (C > 1) {
+            const bool up = lane & BIT;
+#pragma unroll
+            for (int j = 0; j < C / 2; ++j) {
+                const float keep = up ? x[j + C / 2] : x[j], give = up ? x[j] : x[j + C / 2];
+                x[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, BIT));
+            }
+            col_max<C / 2, BIT / 2>(x, lane);
+        } else {
+            x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], BIT));
+            col_max<1, BIT / 2>(x, lane);
+        }
+    }
 }
 
 // One segment: CTA c's tiles of unit u.
@@ -181,10 +192,11 @@ struct Seg {
     int u, rt, kvh, x0, n;   // row tile, KV head, first token tile of the unit, tiles
 };
 
-// The segment's query rows (zero rows behind the last), and fresh references.
-template <int N>
+// The segment's query rows (zero rows behind the last), and fresh references; thread tid of T.
+template <int N, int T>
 __device__ __forceinline__ void load_rows(Smem<N> &s, const Args &a, const Seg &sg, int tid) {
-    for (int e = tid; e < N * 8; e += kThreads) {
+#pragma unroll 1
+    for (int e = tid; e < N * 8; e += T) {
         const int n = e >> 3, w = e & 7, row = sg.rt * N + n;
         uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (row < a.rows) {
@@ -204,8 +216,8 @@ __device__ __forceinline__ void load_rows(Smem<N> &s, const Args &a, const Seg &
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ Args a) {
-    constexpr int C = N / 2;                 // rows of a softmax thread
-    constexpr int CH = C < 32 ? C : 32;      // columns a tensor-memory load
+    constexpr int kP = N == 16 ? 2 : 4;      // softmax groups: parts of the rows
+    constexpr int C = N / kP;                // rows of a softmax thread
     constexpr int kTW = N == 16 ? 1 : 2;     // T warps
     constexpr int kSW = N == 16 ? 2 : 4;     // sum warps
     constexpr uint32_t kColS = 0, kColO = 2 * N, kColK = 3 * N;
@@ -221,9 +233,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     if (warp == 0) {
         // arrivals a phase: k_full 4 (warps), k_empty S and the T warps, kz_full 4, v_full 4,
         // s_full the MMA and the T warps, p_full 8 (warps), o_done O'^T and the sum warps, drain 1
-        constexpr unsigned long long kCounts = 4ull | (1ull + kTW) << 4 | 4ull << 8 |
-                                               4ull << 12 | (1ull + kTW) << 16 | 8ull << 20 | (1ull + kSW) << 24 | 1ull << 28;
-        if (lane < 16) mbar_init(&s.k_full[0] + lane, (uint32_t)(kCounts >> (4 * (lane >> 1))) & 15u);
+        constexpr unsigned long long kCounts = 4ull | (1ull + kTW) << 8 | 4ull << 16 | 4ull << 24 | (1ull + kTW) << 32 |
+                                               (4ull * kP) << 40 | (1ull + kSW) << 48 | 1ull << 56;
+        if (lane < 16) mbar_init(&s.k_full[0] + lane, (uint32_t)(kCounts >> (8 * (lane >> 1))) & 255u);
         fence_mbar_init();
         if (lane == 0) s.abort = 0;
     }
@@ -245,10 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     auto ph = [](int k) { return (uint32_t)(k >> 1) & 1; };
     auto ph_prev = [](int k) { return (uint32_t)((k >> 1) - 1) & 1; };
 
-    // Every role runs the segments in step: the query rows, a block barrier, the
-    // role's own work on the segment's tiles, a block barrier.  (Each role has its
-    // own copy of this loop, behind its own register budget.)
-    auto segments = [&](auto work) {
+    // Every role runs the segments in step: what the role does before (the first
+    // tile's loads, the query rows), a block barrier, the role's work on the
+    // segment's tiles, a block barrier.  (Each role has its own copy of this loop,
+    // behind its own register budget.)
+    auto segments = [&](auto before, auto work) {
         for (int x = lo; x < hi;) {
             Seg sg;
             sg.u = x / a.tab.tpu;
@@ -257,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             sg.x0 = x - sg.u * a.tab.tpu;
             sg.n = min(hi, (sg.u + 1) * a.tab.tpu) - x;
             x += sg.n;
-            load_rows<N>(s, a, sg, tid);
+            before(sg);
             sync_all();
             work(sg);
             it += sg.n;
@@ -268,14 +281,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     };
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-        segments([&](const Seg &sg) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 72;\n");
+        segments([](const Seg &) {}, [&](const Seg &sg) {
             if (warp == 0 || (warp == 2 && kTW == 2)) {
                 // ---------------- T [rows x quarters] = Q [z | s], 16-row tiles MT0 .. MT0 + MT - 1
-                constexpr int MT = N / 16 / kTW, MB = MT < 2 ? MT : 2;   // 16-row tiles of a warp, at a time
+                constexpr int MT = N / 16 / kTW;   // 16-row tiles of a warp
                 const float sc = a.scale_log2;
                 const int lrow = (lane & 7) + 8 * ((lane >> 3) & 1), lch = lane >> 4;
                 const uint32_t qrow = smem_addr(s.q[0]) + ((warp >> 1) * MT * 16 + lrow) * 128;
+                // a 16-row tile's Q, the next one's asked for behind the products (a load takes 400 cycles under MMAs)
+                uint32_t qa[8][4];
+                auto load_q = [&](int m) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        ldmatrix_x4(qa[kk], qrow + m * 2048 + (kk >> 2) * (N * 128) + (((2 * (kk & 3) + lch) ^ (lrow & 7)) << 4));
+                };
+                load_q(0);
                 for (int i = 0; i < sg.n; ++i) {
                     const int k = it + i, st = k & 1;
                     const uint32_t keep = sg.x0 + i < a.nt_packed ? 0xffffffffu : 0u;   // fp16 tokens have no T
@@ -284,36 +305,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     // column g_: z of quarter g_, then s of quarter g_ - 4
                     const uint32_t *col = s.ksz[st][g_ & 3] + (g_ < 4 ? kKszZero : 0) + t_;
                     float *tz = &s.tz[k & 3][2 * (t_ & 1)][(warp >> 1) * MT * 16 + g_];
+                    uint32_t bz[8][2];
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        bz[kk][0] = col[8 * kk] & keep;
+                        bz[kk][1] = col[8 * kk + 4] & keep;
+                    }
 #pragma unroll 1
-                    for (int m0 = 0; m0 < MT; m0 += MB) {
-                        float d[MB][2][4];
+                    for (int m = 0; m < MT; ++m) {
+                        float d[2][4];
 #pragma unroll
-                        for (int e = 0; e < 8 * MB; ++e) (&d[0][0][0])[e] = 0.f;
-#pragma unroll 1
-                        for (int kb = 0; kb < 2; ++kb) {   // 64 channels: every load before the products
-                            uint32_t bz[4][2], qa[MB][4][4];
+                        for (int e = 0; e < 8; ++e) (&d[0][0])[e] = 0.f;
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                bz[kk][0] = col[32 * kb + 8 * kk] & keep;
-                                bz[kk][1] = col[32 * kb + 8 * kk + 4] & keep;
+                        for (int kk = 0; kk < 8; ++kk) mma16816(d[kk & 1], qa[kk], bz[kk][0], bz[kk][1]);
+                        if (MT > 1) load_q(m + 1 < MT ? m + 1 : 0);
 #pragma unroll
-                                for (int m = 0; m < MB; ++m)
-                                    ldmatrix_x4(qa[m][kk], qrow + (m0 + m) * 2048 + kb * (N * 128) +
-                                                               (((2 * kk + lch) ^ (lrow & 7)) << 4));
-                            }
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                                for (int m = 0; m < MB; ++m) mma16816(d[m][kk & 1], qa[m][kk], bz[kk][0], bz[kk][1]);
+                        for (int e = 0; e < 4; ++e) {
+                            float v = d[0][e] + d[1][e];
+                            v += __shfl_xor_sync(0xffffffffu, v, 2);
+                            if (t_ < 2) tz[(e & 1) * N + 16 * m + 8 * (e >> 1)] = v * sc;
                         }
-#pragma unroll
-                        for (int m = 0; m < MB; ++m)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float v = d[m][0][e] + d[m][1][e];
-                                v += __shfl_xor_sync(0xffffffffu, v, 2);
-                                if (t_ < 2) tz[(e & 1) * N + 16 * (m0 + m) + 8 * (e >> 1)] = v * sc;
-                            }
                     }
                     tc::arrive_warp(&s.k_empty[st]);
                     // P and the factors of two tiles ago have been read (waited for here: the softmax warps then wait
@@ -363,25 +374,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             }
         });
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-        segments([&](const Seg &sg) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+        uint4 c0, c1;        // the token's codes
+        uint2 ks, kz;        // four channels of the quarter's group: scale, zero
+        auto fetch = [&](size_t plane, int xt) {
+            const int t = xt * kTile + 32 * quad;   // the warp's first token: all 32 in one group
+            if (xt < a.nt_packed && t < a.n_packed) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.k_codes + (plane * a.cap + t + lane) * 8);
+                c0 = __ldg(src);
+                c1 = __ldg(src + 1);
+                const size_t grow = (plane * (a.cap >> a.lg2G) + (t >> a.lg2G)) * kD;
+                ks = __ldg(reinterpret_cast<const uint2 *>(a.k_scale + grow) + lane);
+                kz = __ldg(reinterpret_cast<const uint2 *>(a.k_zero + grow) + lane);
+            }
+        };
+        segments([&](const Seg &sg) { fetch(sg.kvh, sg.x0); }, [&](const Seg &sg) {
             // ---------------- K: token 32 quad + lane of the tile
             const size_t plane = (size_t)sg.kvh;
             const Offset off(false);
-            uint4 c0, c1;        // the token's codes
-            uint2 ks, kz;        // four channels of the quarter's group: scale, zero
-            auto fetch = [&](int xt) {
-                const int t = xt * kTile + 32 * quad;   // the warp's first token: all 32 in one group
-                if (xt < a.nt_packed && t < a.n_packed) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(a.k_codes + (plane * a.cap + t + lane) * 8);
-                    c0 = __ldg(src);
-                    c1 = __ldg(src + 1);
-                    const size_t grow = (plane * (a.cap >> a.lg2G) + (t >> a.lg2G)) * kD;
-                    ks = __ldg(reinterpret_cast<const uint2 *>(a.k_scale + grow) + lane);
-                    kz = __ldg(reinterpret_cast<const uint2 *>(a.k_zero + grow) + lane);
-                }
-            };
-            fetch(sg.x0);
             for (int i = 0; i < sg.n; ++i) {
                 const int k = it + i, st = k & 1, xt = sg.x0 + i;
                 const bool packed = xt < a.nt_packed;
@@ -395,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 got.x = __shfl_xor_sync(0xffffffffu, give.x, 2);
                 got.y = __shfl_xor_sync(0xffffffffu, give.y, 2);
                 const uint2 a0 = up ? got : mine, b0 = up ? mine : got;
-                fetch(xt + 1);
+                fetch(plane, xt + 1);
                 if (k >= 2 && !wait_warp(s, &s.k_empty[st], ph_prev(k))) break;
                 tc::fence_after_sync();
                 *reinterpret_cast<uint4 *>(sz + (up ? kKszZero : 0) + 8 * (lane >> 2) + 4 * (lane & 1)) =
@@ -450,24 +460,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         });
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-        segments([&](const Seg &sg) {
+        const int r = 32 * quad + lane;
+        uint4 c0, c1;
+        uint32_t vs = 0, vz = 0;
+        auto fetch = [&](size_t plane, int xt) {
+            const int t = xt * kTile + r;
+            if (xt < a.nt_packed && t < a.n_packed) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.v_codes + (plane * a.cap + t) * 8);
+                c0 = __ldg(src);
+                c1 = __ldg(src + 1);
+                vs = __ldg(a.v_scale + plane * a.cap + t);
+                vz = __ldg(a.v_zero + plane * a.cap + t);
+            }
+        };
+        segments([&](const Seg &sg) { fetch(sg.kvh, sg.x0); }, [&](const Seg &sg) {
             // ---------------- V: token 32 quad + lane of the tile
             const size_t plane = (size_t)sg.kvh;
-            const int r = 32 * quad + lane;
             const Offset off(lane & 1);
-            uint4 c0, c1;
-            uint32_t vs = 0, vz = 0;
-            auto fetch = [&](int xt) {
-                const int t = xt * kTile + r;
-                if (xt < a.nt_packed && t < a.n_packed) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(a.v_codes + (plane * a.cap + t) * 8);
-                    c0 = __ldg(src);
-                    c1 = __ldg(src + 1);
-                    vs = __ldg(a.v_scale + plane * a.cap + t);
-                    vz = __ldg(a.v_zero + plane * a.cap + t);
-                }
-            };
-            fetch(sg.x0);
             for (int i = 0; i < sg.n; ++i) {
                 const int k = it + i, st = k & 1, xt = sg.x0 + i;
                 const bool packed = xt < a.nt_packed;
@@ -478,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 const uint32_t s2 = vs * 0x00010001u;
                 const float zs = live && packed ? fmaf(lane & 1 ? 2.f : 1.f, h2f((uint16_t)vs), h2f((uint16_t)vz)) : 0.f;
                 const uint16_t zh = f2h(zs), zl = f2h(zs - h2f(zh));
-                fetch(xt + 1);
+                fetch(plane, xt + 1);
                 if (k >= 2 && !wait_warp(s, &s.o_done[st], ph_prev(k))) break;
                 reinterpret_cast<uint16_t *>(s.vz[st][0])[r] = zh;
                 reinterpret_cast<uint16_t *>(s.vz[st][1])[r] = zl;
@@ -521,11 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 tc::arrive_warp(&s.v_full[st]);
             }
         });
-    } else if (warp < 20) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
-        segments([&](const Seg &sg) {
+    } else if (warp < 28) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+        segments([&](const Seg &sg) { load_rows<N, 512>(s, a, sg, tid - 384); }, [&](const Seg &sg) {
+            if (warp >= 12 + 4 * kP) return;
             // ---------------- softmax: token lane r, rows n0 .. n0 + C - 1
-            const int half = warp >= 16, n0 = half * C, r = 32 * quad + lane, bar = 1 + half;
+            const int half = (warp - 12) >> 2, n0 = half * C, r = 32 * quad + lane, bar = 1 + half;
             const float sc = 2.f * a.scale_log2;
             float *bias = s.bias[warp - 12];
             bool ok = true;
@@ -539,37 +549,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 const uint32_t ts = tmem + lanes + kColS + st * N + n0;
                 const unsigned long long sc2 = f2pack(sc, sc);
                 // the tile's log2 scores relative to the references; a second time if these move
-                // (C = 64: 32 at a time and read twice, so that the loop stays in the instruction cache)
-                float x[CH];
-                auto fetch = [&](int j0) { tc::tmem_ld<CH>(ts + j0, *reinterpret_cast<uint32_t(*)[CH]>(&x[0])); };
-                auto arrived = [&](int j0) {
-                    tc::wait_ld();
-#pragma unroll
-                    for (int j = 0; j < CH; j += 4) {
-                        const float4 b4 = *reinterpret_cast<const float4 *>(&bias[j0 + j]);
-                        f2unpack(ffma2(f2pack(x[j], x[j + 1]), sc2, f2pack(b4.x, b4.y)), x[j], x[j + 1]);
-                        f2unpack(ffma2(f2pack(x[j + 2], x[j + 3]), sc2, f2pack(b4.z, b4.w)), x[j + 2], x[j + 3]);
-                    }
-                };
+                float x[C];
                 bool moved = false, aborted = false;
                 for (;;) {
-                    fetch(0);
+                    tc::tmem_ld<C>(ts, *reinterpret_cast<uint32_t(*)[C]>(&x[0]));
                     for (int j = lane; j < C; j += 32) bias[j] = s.tz[k & 3][quad][n0 + j] - s.m[n0 + j];
                     __syncwarp();
                     float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll 1
-                    for (int j0 = 0; j0 < C; j0 += CH) {
-                        if (j0) fetch(j0);
-                        arrived(j0);
+                    tc::wait_ld();
 #pragma unroll
-                        for (int j = 0; j < CH; j += 4) {
-                            mx0 = max3(mx0, x[j], x[j + 1]);
-                            mx1 = max3(mx1, x[j + 2], x[j + 3]);
-                        }
+                    for (int j = 0; j < C; j += 4) {
+                        const float4 b4 = *reinterpret_cast<const float4 *>(&bias[j]);
+                        f2unpack(ffma2(f2pack(x[j], x[j + 1]), sc2, f2pack(b4.x, b4.y)), x[j], x[j + 1]);
+                        f2unpack(ffma2(f2pack(x[j + 2], x[j + 3]), sc2, f2pack(b4.z, b4.w)), x[j + 2], x[j + 3]);
+                        mx0 = max3(mx0, x[j], x[j + 1]);
+                        mx1 = max3(mx1, x[j + 2], x[j + 3]);
                     }
                     // does a score pass its row's reference by kLazy?  (a failed wait joins the vote: the
                     // warps of a half leave the loop together, at this barrier)
-                    if (moved || !or_over(bar, !ok || i == 0 || (live && fmaxf(mx0, mx1) > kLazy))) break;
+                    if (moved || (i > 0 && !or_over(bar, !ok || (live && fmaxf(mx0, mx1) > kLazy)))) break;
                     moved = true;
                     if (or_over(bar, !ok)) {
                         ok = false;
@@ -577,17 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                         break;
                     }
                     // column maxima of the tile -> new references; the sums and O'^T follow
-#pragma unroll 1
-                    for (int j0 = 0; j0 < C; j0 += 8) {
-                        uint32_t y[8];
-                        tc::tmem_ld<8>(ts + j0, y);
-                        tc::wait_ld();
+                    if (!live)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float top = warp_max(live ? fmaf(__uint_as_float(y[j]), sc, bias[j0 + j]) : -INFINITY);
-                            if (lane == j) s.wmax[quad][n0 + j0 + j] = top;
-                        }
-                    }
+                        for (int j = 0; j < C; ++j) x[j] = -INFINITY;
+                    col_max<C, 16>(x, lane);
+                    s.wmax[quad][n0 + lane / (32 / C)] = x[0];
                     sync_half(bar);
                     if (r < C) {
                         const int n = n0 + r;
@@ -622,20 +614,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 if (r == 0) s.resc[st][half] = moved;
                 const uint32_t live2 = live ? 0xffffffffu : 0u;
                 unsigned char *row = reinterpret_cast<unsigned char *>(s.p[st][n0 >> 6]) + r * 128;
-#pragma unroll 1
-                for (int j0 = 0; j0 < C; j0 += CH) {
-                    if (C > CH) {
-                        fetch(j0);
-                        arrived(j0);
-                    }
 #pragma unroll
-                    for (int j = 0; j < CH; j += 8) {
-                        uint32_t w[4];
+                for (int j = 0; j < C; j += 8) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] = pack_half2(ex2(x[j + 2 * e]), ex2(x[j + 2 * e + 1])) & live2;
-                        *reinterpret_cast<uint4 *>(row + (((((n0 + j0 + j) & 63) >> 3) ^ (r & 7)) << 4)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int e = 0; e < 4; ++e) w[e] = pack_half2(ex2(x[j + 2 * e]), ex2(x[j + 2 * e + 1])) & live2;
+                    *reinterpret_cast<uint4 *>(row + (((((n0 + j) & 63) >> 3) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 tc::fence_proxy_async_smem();
                 tc::fence_before_sync();
@@ -644,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             // ---------------- epilogue: the segment's state to slot c + u
             const int last = it + sg.n - 1;
             if (ok) ok = wait_warp(s, &s.o_done[last & 1], ph(last));
-            asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(3 + half), "n"(128 + 16 * kSW) : "memory");   // the sums are in s.l, s.pz
+            asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(5 + half), "n"(160) : "memory");   // the sums are in s.l, s.pz
             if (ok) {
                 tc::fence_after_sync();
                 float *base = a.part + (size_t)(c + sg.u) * N * kPreStride;
@@ -670,13 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             tc::fence_before_sync();
         });
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-        segments([&](const Seg &sg) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+        segments([](const Seg &) {}, [&](const Seg &sg) {
             // ---------------- sums over P: [1; hi; lo] P, rows g_ = 0, 1, 2 of the product, for rows n0 .. n0 + 8 NT - 1
             constexpr int NT = N / 8 / kSW;   // 8-row tiles of a warp
             constexpr int KB = NT < 2 ? 8 : 16 / NT;   // 16-token steps whose loads go out together
             if (quad < kSW) {
-                const int n0 = quad * NT * 8, half = quad / (kSW / 2);
+                const int n0 = quad * NT * 8, half = quad;
                 float total[NT][2];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) total[j][0] = total[j][1] = 0.f;
@@ -739,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     }
                 }
                 __syncwarp();
-                asm volatile("barrier.cta.arrive %0, %1;\n" ::"r"(3 + half), "n"(128 + 16 * kSW) : "memory");   // to the half's epilogue
+                asm volatile("barrier.cta.arrive %0, %1;\n" ::"r"(5 + half), "n"(160) : "memory");   // to the half's epilogue
             }
         });
     }
