@@ -66,14 +66,14 @@ struct Smem {
     uint16_t v[2][2][kTile * 64];       // [stage][64-channel block][token][64], 128-byte swizzle
     uint16_t p[2][kNB][kTile * 64];     // [stage][64-row block][token][64]
     uint16_t q[2][N * 64];              // [64-channel block][row][64]
-    uint32_t ksz[2][4][kKszStride];     // [stage][quarter]: scale pairs [64], zero pairs [64] of its key group
+    uint32_t ksz[4][4][kKszStride];     // [tile & 3][quarter]: scale pairs [64], zero pairs [64] of its key group
     uint32_t vz[2][2][kTile / 2];       // [stage][hi, lo]: fp16 z + o s of the value tokens
     float tz[4][4][N];                  // [tile & 3][quarter][row]: T in log2 units
     float bias[16][N / 2];               // a softmax warp's T - reference of the tile in hand
     float m[N], alpha[2][N], l[N], pz[N];
     float wmax[4][N];
     int resc[2][4];                     // [stage][part]: the tile moved the references (alpha holds the factors)
-    uint64_t k_full[2], k_empty[2], kz_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain[2];   // in this order
+    uint64_t k_full[2], k_empty[2], kz_full[4], v_full[2], s_full[2], p_full[2], o_done[2], drain[2];   // in this order
     uint32_t tmem_base;
     int abort;
 };
@@ -231,11 +231,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const int c = blockIdx.x;
 
     if (warp == 0) {
-        // arrivals a phase: k_full 4 (warps), k_empty S and the T warps, kz_full 4, v_full 4,
-        // s_full the MMA and the T warps, p_full 8 (warps), o_done O'^T and the sum warps, drain 1
-        constexpr unsigned long long kCounts = 4ull | (1ull + kTW) << 8 | 4ull << 16 | 4ull << 24 | (1ull + kTW) << 32 |
-                                               (4ull * kP) << 40 | (1ull + kSW) << 48 | 1ull << 56;
-        if (lane < 16) mbar_init(&s.k_full[0] + lane, (uint32_t)(kCounts >> (8 * (lane >> 1))) & 255u);
+        // arrivals a phase: k_full 4 (warps), k_empty S and the T warps, kz_full 4 (four barriers), v_full 4, s_full the
+        // MMA and the T warps, p_full the softmax warps, o_done O'^T and the sum warps, drain 1
+        constexpr unsigned long long kLow = 4ull | (1ull + kTW) << 8 | 4ull << 16 | 4ull << 24 | 4ull << 32 |
+                                            (1ull + kTW) << 40 | (4ull * kP) << 48 | (1ull + kSW) << 56;
+        if (lane < 18) mbar_init(&s.k_full[0] + lane, lane < 16 ? (uint32_t)(kLow >> (8 * (lane >> 1))) & 255u : 1u);
         fence_mbar_init();
         if (lane == 0) s.abort = 0;
     }
@@ -301,9 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     const int k = it + i, st = k & 1;
                     const uint32_t keep = sg.x0 + i < a.nt_packed ? 0xffffffffu : 0u;   // fp16 tokens have no T
                     // (tz of four tiles ago has been read: K of this tile came after S of two ago, which came after P of four)
-                    if (!wait_warp(s, &s.kz_full[st], ph(k))) break;
+                    if (!wait_warp(s, &s.kz_full[k & 3], (uint32_t)(k >> 2) & 1)) break;
                     // column g_: z of quarter g_, then s of quarter g_ - 4
-                    const uint32_t *col = s.ksz[st][g_ & 3] + (g_ < 4 ? kKszZero : 0) + t_;
+                    const uint32_t *col = s.ksz[k & 3][g_ & 3] + (g_ < 4 ? kKszZero : 0) + t_;
                     float *tz = &s.tz[k & 3][2 * (t_ & 1)][(warp >> 1) * MT * 16 + g_];
                     uint32_t bz[8][2];
 #pragma unroll
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             for (int i = 0; i < sg.n; ++i) {
                 const int k = it + i, st = k & 1, xt = sg.x0 + i;
                 const bool packed = xt < a.nt_packed;
-                uint32_t *sz = s.ksz[st][quad];
+                uint32_t *sz = s.ksz[k & 3][quad];
                 const int t = (packed ? xt : xt - a.nt_packed) * kTile + 32 * quad;
                 uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
                 // lanes of channels 16w + 0..7 pair the scales, those of 16w + 8..15 the zeros
@@ -406,29 +406,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 got.y = __shfl_xor_sync(0xffffffffu, give.y, 2);
                 const uint2 a0 = up ? got : mine, b0 = up ? mine : got;
                 fetch(plane, xt + 1);
-                if (k >= 2 && !wait_warp(s, &s.k_empty[st], ph_prev(k))) break;
-                tc::fence_after_sync();
+                // (T of four tiles ago has read its scales: the wait below was for T of three ago, a tile ago)
                 *reinterpret_cast<uint4 *>(sz + (up ? kKszZero : 0) + 8 * (lane >> 2) + 4 * (lane & 1)) =
                     make_uint4(__byte_perm(a0.x, b0.x, 0x5410), __byte_perm(a0.x, b0.x, 0x7632),
                                __byte_perm(a0.y, b0.y, 0x5410), __byte_perm(a0.y, b0.y, 0x7632));
-                tc::arrive_warp(&s.kz_full[st]);
+                tc::arrive_warp(&s.kz_full[k & 3]);
+                if (k >= 2 && !wait_warp(s, &s.k_empty[st], ph_prev(k))) break;
+                tc::fence_after_sync();
                 const uint32_t dst = tmem + lanes + kColK + st * 64;
                 if (packed && t < a.n_packed) {
                     uint32_t d = dst;
                     const uint32_t *sp = sz;
-#pragma unroll 1
-                    for (int wi = 0; wi < 8; wi += 2, sp += 16, d += 16) {   // two words an iteration, then the next two move down
-                        uint4 sv4[4];
+                    // two words an iteration, each one's scales asked for a word ahead (behind the last word: the zeros)
+                    uint4 sv[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) sv4[j] = *reinterpret_cast<const uint4 *>(sp + 4 * j);
-                        uint32_t out[16];
+                    for (int j = 0; j < 4; ++j) sv[j] = *reinterpret_cast<const uint4 *>(sp + 4 * j);
+#pragma unroll 1
+                    for (int wi = 0; wi < 4; ++wi, d += 16) {
+                        sp += 16;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const uint4 s0 = sv4[2 * j], s1 = sv4[2 * j + 1];
-                            const uint32_t sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-                            dequant_word(w[j], off, [&](int i2) { return sv[i2]; }, out + 8 * j);
+                            const uint4 s0 = sv[2 * j], s1 = sv[2 * j + 1];
+                            const uint32_t pair[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                            uint32_t out[8];
+                            dequant_word(w[j], off, [&](int i2) { return pair[i2]; }, out);
+                            tc::tmem_st<8>(d + 8 * j, out);
+                            sv[2 * j] = *reinterpret_cast<const uint4 *>(sp + 8 * j);
+                            sv[2 * j + 1] = *reinterpret_cast<const uint4 *>(sp + 8 * j + 4);
                         }
-                        tc::tmem_st<16>(d, out);
 #pragma unroll
                         for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
                     }
@@ -445,12 +450,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     const uint4 *src =
                         reinterpret_cast<const uint4 *>(a.k_res + (plane * a.ring + (i0 < a.n_res ? slot : 0)) * kD);
 #pragma unroll 1
-                    for (int wi = 0; wi < 8; ++wi) {
-                        uint32_t out[8];
-                        pair_order(__ldg(src + 2 * wi), __ldg(src + 2 * wi + 1), out);
+                    for (int w0 = 0; w0 < 8; w0 += 2) {   // two words in flight
+                        uint4 x[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) out[e] = i0 < a.n_res ? hmul2(out[e], kHalf2) : 0u;
-                        tc::tmem_st<8>(dst + 8 * wi, out);
+                        for (int j = 0; j < 4; ++j) x[j] = __ldg(src + 2 * w0 + j);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t out[8];
+                            pair_order(x[2 * j], x[2 * j + 1], out);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) out[e] = i0 < a.n_res ? hmul2(out[e], kHalf2) : 0u;
+                            tc::tmem_st<8>(dst + 8 * (w0 + j), out);
+                        }
                     }
                 }
                 tc::wait_st();
@@ -518,12 +529,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     if (slot >= a.ring) slot -= a.ring;
                     const uint4 *src = reinterpret_cast<const uint4 *>(a.v_res + (plane * a.ring + (live ? slot : 0)) * kD);
 #pragma unroll 1
-                    for (int wi = 0; wi < 8; ++wi) {
-                        uint32_t out[8];
-                        pair_order(__ldg(src + 2 * wi), __ldg(src + 2 * wi + 1), out);
+                    for (int w0 = 0; w0 < 8; w0 += 2) {
+                        uint4 x[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) out[e] = live ? hmul2(out[e], kHalf2) : 0u;
-                        put(wi, out);
+                        for (int j = 0; j < 4; ++j) x[j] = __ldg(src + 2 * w0 + j);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t out[8];
+                            pair_order(x[2 * j], x[2 * j + 1], out);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) out[e] = live ? hmul2(out[e], kHalf2) : 0u;
+                            put(w0 + j, out);
+                        }
                     }
                 }
                 tc::fence_proxy_async_smem();
