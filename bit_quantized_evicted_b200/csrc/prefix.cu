@@ -32,15 +32,25 @@
 // Dequantization: c | 0x6400 is the fp16 number 1024 + c (code bits at mantissa
 // bit 2I: 1024 + 4^I c); one fma makes it (c - o) / 2, one product (c - o) s / 2.
 //
-// The loops are kept short on purpose: with the five roles unrolled over their
-// tiles, 7.7 of 14 warps waited for instructions (N = 64; 3.3 us a tile).
+// 32 warps: 0 and 2 compute T (half of the rows each), 1 and 3 issue the MMAs of
+// the two products, 4-7 dequantize K, 8-11 V (a thread a token), 12-27 softmax
+// (thread = token lane, a quarter of the rows each; N = 16: two halves, 20-27
+// idle), 28-31 the sums over P (a quarter of the rows each).  S, K', V' and P
+// have two buffers.  The reference max of a row moves only when a score passes it
+// by 2^8; then the column maxima of a part's four warps meet in shared memory and
+// O'^T and the sums are rescaled.
 //
-// 24 warps: 0 and 2 compute T (half of the rows each), 1 and 3 issue the
-// MMAs of the two products, 4-7 dequantize K, 8-11 V (a thread a token), 12-19 softmax (thread = token lane,
-// half of the rows each), 20-23 the sums over P (a quarter of the rows each).  S, K', V' and P have two
-// buffers.  The reference max of a row moves only when a score passes it by 2^8;
-// then the column maxima of a half's four warps meet in shared memory and O'^T
-// and the sums are rescaled.
+// What bounds it: the roles' chains of short dependent steps, at about 0.6
+// instructions a cycle and SM quarter.  Under running MMAs a shared-memory load
+// takes 200-400 cycles and a wait that is over 250, so the softmax warps wait
+// once a tile and loads are asked for ahead (one wait instead of three: 461 -> 437
+// us a step at 96 sequences x 131000 tokens; 16 softmax warps instead of 8, with
+// every score in registers: 437 -> 402).  The loops are kept short on purpose:
+// with the roles unrolled over their tiles, half of the warps waited for
+// instructions (3.3 us a tile at N = 64, now 1.5).  The pass takes 21 us behind
+// 4321 tokens (24 sequences, 32 KV heads, N = 32), 34 us behind 32768 (16
+// sequences, N = 64) and 345 us behind 131000 (96 sequences, three tiles of 128
+// rows: 600 TFLOP/s).
 #include <math.h>
 
 #include <mutex>
@@ -66,14 +76,14 @@ struct Smem {
     uint16_t v[2][2][kTile * 64];       // [stage][64-channel block][token][64], 128-byte swizzle
     uint16_t p[2][kNB][kTile * 64];     // [stage][64-row block][token][64]
     uint16_t q[2][N * 64];              // [64-channel block][row][64]
-    uint32_t ksz[4][4][kKszStride];     // [tile & 3][quarter]: scale pairs [64], zero pairs [64] of its key group
+    uint32_t ksz[8][4][kKszStride];     // [tile & 7][quarter]: scale pairs [64], zero pairs [64] of its key group
     uint32_t vz[2][2][kTile / 2];       // [stage][hi, lo]: fp16 z + o s of the value tokens
     float tz[4][4][N];                  // [tile & 3][quarter][row]: T in log2 units
-    float bias[16][N / 2];               // a softmax warp's T - reference of the tile in hand
+    float bias[16][N / 2];              // a softmax warp's T - reference of the tile in hand
     float m[N], alpha[2][N], l[N], pz[N];
     float wmax[4][N];
     int resc[2][4];                     // [stage][part]: the tile moved the references (alpha holds the factors)
-    uint64_t k_full[2], k_empty[2], kz_full[4], v_full[2], s_full[2], p_full[2], o_done[2], drain[2];   // in this order
+    uint64_t k_full[2], k_empty[2], kz_full[8], v_full[2], s_full[2], p_full[2], o_done[2], drain[2];   // in this order
     uint32_t tmem_base;
     int abort;
 };
@@ -231,11 +241,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const int c = blockIdx.x;
 
     if (warp == 0) {
-        // arrivals a phase: k_full 4 (warps), k_empty S and the T warps, kz_full 4 (four barriers), v_full 4, s_full the
-        // MMA and the T warps, p_full the softmax warps, o_done O'^T and the sum warps, drain 1
-        constexpr unsigned long long kLow = 4ull | (1ull + kTW) << 8 | 4ull << 16 | 4ull << 24 | 4ull << 32 |
-                                            (1ull + kTW) << 40 | (4ull * kP) << 48 | (1ull + kSW) << 56;
-        if (lane < 18) mbar_init(&s.k_full[0] + lane, lane < 16 ? (uint32_t)(kLow >> (8 * (lane >> 1))) & 255u : 1u);
+        // arrivals a phase: k_full 4 (warps), k_empty S, kz_full 4 (eight barriers), v_full 4, s_full S and the T warps,
+        // p_full the softmax warps, o_done O'^T and the sum warps, drain 1
+        constexpr unsigned long long kCounts = 4ull | 1ull << 8 | 4ull << 16 | 4ull << 24 | (1ull + kTW) << 32 |
+                                               (4ull * kP) << 40 | (1ull + kSW) << 48 | 1ull << 56;
+        const int kind = lane < 4 ? lane >> 1 : lane < 12 ? 2 : (lane >> 1) - 3;
+        if (lane < 22) mbar_init(&s.k_full[0] + lane, (uint32_t)(kCounts >> (8 * kind)) & 255u);
         fence_mbar_init();
         if (lane == 0) s.abort = 0;
     }
@@ -300,10 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 for (int i = 0; i < sg.n; ++i) {
                     const int k = it + i, st = k & 1;
                     const uint32_t keep = sg.x0 + i < a.nt_packed ? 0xffffffffu : 0u;   // fp16 tokens have no T
-                    // (tz of four tiles ago has been read: K of this tile came after S of two ago, which came after P of four)
-                    if (!wait_warp(s, &s.kz_full[k & 3], (uint32_t)(k >> 2) & 1)) break;
+                    // (tz of four tiles ago has been read: the last tile's wait below was for P of three ago)
+                    if (!wait_warp(s, &s.kz_full[k & 7], (uint32_t)(k >> 3) & 1)) break;
                     // column g_: z of quarter g_, then s of quarter g_ - 4
-                    const uint32_t *col = s.ksz[k & 3][g_ & 3] + (g_ < 4 ? kKszZero : 0) + t_;
+                    const uint32_t *col = s.ksz[k & 7][g_ & 3] + (g_ < 4 ? kKszZero : 0) + t_;
                     float *tz = &s.tz[k & 3][2 * (t_ & 1)][(warp >> 1) * MT * 16 + g_];
                     uint32_t bz[8][2];
 #pragma unroll
@@ -326,7 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                             if (t_ < 2) tz[(e & 1) * N + 16 * m + 8 * (e >> 1)] = v * sc;
                         }
                     }
-                    tc::arrive_warp(&s.k_empty[st]);
                     // P and the factors of two tiles ago have been read (waited for here: the softmax warps then wait
                     // once a tile, and a wait that is over takes 250 cycles)
                     if (k >= 2 && !wait_warp(s, &s.o_done[st], ph_prev(k))) break;
@@ -395,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             for (int i = 0; i < sg.n; ++i) {
                 const int k = it + i, st = k & 1, xt = sg.x0 + i;
                 const bool packed = xt < a.nt_packed;
-                uint32_t *sz = s.ksz[k & 3][quad];
+                uint32_t *sz = s.ksz[k & 7][quad];
                 const int t = (packed ? xt : xt - a.nt_packed) * kTile + 32 * quad;
                 uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
                 // lanes of channels 16w + 0..7 pair the scales, those of 16w + 8..15 the zeros
@@ -406,11 +416,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 got.y = __shfl_xor_sync(0xffffffffu, give.y, 2);
                 const uint2 a0 = up ? got : mine, b0 = up ? mine : got;
                 fetch(plane, xt + 1);
-                // (T of four tiles ago has read its scales: the wait below was for T of three ago, a tile ago)
+                // (T of eight tiles ago is done with its scales: the last tile's wait below was for S of three ago, S comes
+                // after P of two tiles before it, and P after its tile's T: that is T of five ago)
                 *reinterpret_cast<uint4 *>(sz + (up ? kKszZero : 0) + 8 * (lane >> 2) + 4 * (lane & 1)) =
                     make_uint4(__byte_perm(a0.x, b0.x, 0x5410), __byte_perm(a0.x, b0.x, 0x7632),
                                __byte_perm(a0.y, b0.y, 0x5410), __byte_perm(a0.y, b0.y, 0x7632));
-                tc::arrive_warp(&s.kz_full[k & 3]);
+                tc::arrive_warp(&s.kz_full[k & 7]);
                 if (k >= 2 && !wait_warp(s, &s.k_empty[st], ph_prev(k))) break;
                 tc::fence_after_sync();
                 const uint32_t dst = tmem + lanes + kColK + st * 64;
