@@ -250,3 +250,25 @@ def test_expired_waits_are_reported():
     ref = _expected(cache, prefix, None, q, kn, vn)
     _check(mk.decode_attn_prefix(cache, prefix, q, kn, vn, ws=ws), ref)
     assert mk.decode_attn_prefix_status(ws, 20, 8, 2) == 0
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,n", [(2, 8, 8, 60000), (12, 8, 4, 100001), (32, 16, 4, 100000)])
+def test_many_tiles_a_cta(B, Hq, Hkv, n):
+    """More than 20 tiles a CTA: every buffer and barrier goes round several times (16, 32 and 128 rows)."""
+    cache, prefix = _batch([40] * B, Hq, Hkv, "uniform"), _prefix(Hkv, n, 128, 128)
+    q, kn, vn = _inputs(B, Hq, Hkv, 0)
+    some = sorted({0, B // 2, B - 1})
+    g = Hq // Hkv
+    own = {(b, h): cache_rows(cache, b, h) for b in some for h in range(Hkv)}
+    out = mk.decode_attn_prefix(cache, prefix, q, kn, vn)
+    for h in range(Hkv):
+        pk, pv = cache_rows(prefix, 0, h)
+        for b in some:
+            k, v = (torch.cat([p, o, x[b, h:h + 1].double().cpu()]) for p, o, x in
+                    ((pk, own[b, h][0], kn), (pv, own[b, h][1], vn)))
+            qq = q[b, h * g:(h + 1) * g].double().cpu()
+            ref = attend(qq, k, v, TAU)
+            e = 2 ** -11 * TAU * float((qq.abs() @ pk.abs().T).max())
+            mean = attend(qq, k, v.abs(), TAU)
+            tol = 2 ** -11 * ref.abs() + (2 ** -10 + 2 * e) * mean + (2 ** -25 * n + 2e-4) * v.abs().max()
+            _check(out[b, h * g:(h + 1) * g], (ref, tol))
