@@ -283,7 +283,8 @@ struct ArgsDevWin : ArgsDev {
 };
 // ---- a batch behind a shared prefix: each mode's arguments with the prefix pass's partials.  Such a launch follows
 // the prefix pass, which lets it start once all that came before is done: it waits for the pass itself only before
-// it merges the pass's states (at least one unit does: else the pass is not run).
+// it merges the pass's states (at least one unit does: else the pass is not run, P = 0, and the launch waits at its
+// start like the others).
 struct ArgsUniPre : ArgsUni {
     static constexpr bool kPre = true;
     PreTab pre;
@@ -296,6 +297,11 @@ struct ArgsDevPre : ArgsDev {
     static constexpr bool kPre = true;
     PreTab pre;
 };
+template <class A>
+__device__ __forceinline__ bool follows_prefix_pass(const A &a) {
+    if constexpr (A::kPre) return a.pre.P != 0;
+    else return false;
+}
 __device__ __forceinline__ WinSeq s_win(const ArgsUniWin &a, int) { return a.win; }
 __device__ __forceinline__ WinSeq s_win(const ArgsVarWin &a, int b) { return a.win[b]; }
 __device__ __forceinline__ WinSeq s_win(const ArgsDevWin &a, int b) {
@@ -458,7 +464,26 @@ __host__ __device__ constexpr int pair_pos(int i) { return i < 5 ? 2 * i : 2 * (
 // does) and 2^(24 - pos) (value output scale)
 __host__ __device__ constexpr float pair_wq(int i) { return 1.f / (float)(1 << pair_pos(i)); }
 __host__ __device__ constexpr float pair_wo(int i) { return (float)(1 << (24 - pair_pos(i))); }
+// Windowed calls take the value codes through one product with 2^10, which makes
+// normal numbers of them.  The tensor cores align a sum by the operands' exponent
+// fields, and a subnormal's says 2^-14 whatever its leading zeros are: sums over
+// thousands of tokens come out short by some 1e-4 of the (large, positive) sum of
+// p c, which the zero points then cancel.  Error against 64 bits, relative to the
+// output: 3.6e-4 without, 2.1e-4 (the output's own rounding) with it at 4100
+// visible tokens; 24.5 -> 25.5 us there, 152.6 -> 154.0 for 48 sequences without
+// grouping.  (The same for the key codes changes nothing: short sums of both signs.)
+constexpr float kCodeUp = 1024.f;
+__device__ __forceinline__ uint32_t code_up(uint32_t x) {
+    uint32_t y;
+    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(x), "r"(0x64006400u));
+    return y;
+}
 constexpr float kScoreUnit = 16777216.f;   // packed scores come out as code q s 2^-24
+
+// is one of four halves (a, b: pairs) 128 or more in size, or NaN?
+__device__ __forceinline__ bool large_halves(uint32_t a, uint32_t b) {
+    return (((a & 0x7FFF7FFFu) + 0x28002800u) | ((b & 0x7FFF7FFFu) + 0x28002800u)) & 0x80008000u;
+}
 
 // row of packed token j (0..31) in a stage's code block: tokens 2m of a
 // 16-token tile (and 2m+1) land in distinct bank groups, and so do tokens 4t+o
@@ -536,7 +561,7 @@ __device__ void finish_unit(const A &a, Smem &sm, const Seg &s, const WinSeq &w,
     if constexpr (A::kPre) {
         // the row's states over the shared prefix, from the pass before this kernel
         const PreTab &t = a.pre;
-        const int place = t.listed ? t.place[b] : b;
+        const int place = t.P == 0 ? -1 : t.listed ? t.place[b] : b;
         if (place >= 0) wait_prior_grid();   // the prefix pass (this kernel did not wait for it at its start)
         if (place >= 0 && h < a.g) {
             const int row = place * a.g + h, pu = (row >> t.lgN) * a.Hkv + kvh, n = row & ((1 << t.lgN) - 1);
@@ -734,7 +759,9 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
         sm.next = xlo + kWarps * (kStages - 1);   // the first kStages-1 items of each warp are fixed
         seg_info(a, c, xlo, xhi, sm.seg);
     }
-    if (kWait && !A::kPre) wait_prior_grid();
+    if constexpr (kWait) {
+        if (!follows_prefix_pass(a)) wait_prior_grid();
+    }
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue_next();
     __syncthreads();
@@ -786,7 +813,8 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
         float m_ref = -INFINITY, l = 0.f, pz = 0.f;
-        bool vunit = false;   // acc holds packed-value units (x 2^(pos-24)) once a packed item was seen
+        constexpr float vup = A::kWin ? kCodeUp : 1.f;
+        bool vunit = false;   // acc holds packed-value units (x 2^(pos-24) vup) once a packed item was seen
         uint32_t qb = 0;      // this segment's q buffer (shared address)
 
         while (xq0 < sg.hi) {
@@ -908,7 +936,7 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
                     vunit = true;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float f = 1.f / pair_wo(i);
+                        const float f = vup / pair_wo(i);
                         acc[i][0] *= f;
                         acc[i][1] *= f;
                         acc[i][2] *= f;
@@ -975,7 +1003,12 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
                     for (int i = 0; i < 4; ++i) xv[i] = (A::kWin && (hid >> i & 1)) ? -INFINITY : fmaf(sc[i], sl2w, bias);
                 }
                 const float mx = fmaxf(fmaxf(xv[0], xv[1]), fmaxf(xv[2], xv[3]));
-                if (__any_sync(0xffffffffu, mx > kLazy)) {
+                // p * v_scale is rounded to fp16, which holds 2^kLazy times a scale below 2^8: with a larger one
+                // among the lane's tokens the reference keeps up with every score
+                bool move = mx > kLazy;
+                if constexpr (A::kWin || A::kPre)
+                    move = move || (mx > 0.f && large_halves(lds32(S + kOffVs + 4 * g_), lds32(S + kOffVs + 32 + 4 * g_)));
+                if (__any_sync(0xffffffffu, move)) {
                     float xa[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) xa[i] = (A::kWin && (hid >> i & 1)) ? -INFINITY : fmaf(sc[i], sl2w, zcs);
@@ -1026,8 +1059,9 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
                     const uint32_t l1r = shr10(l1), h1r = shr10(h1), l2r = shr10(l2), h2r = shr10(h2);
 #define VSTEP(NU)                                                                   \
     {                                                                               \
-        const uint32_t af[4] = {code_pair<NU>(l1, l1r), code_pair<NU>(h1, h1r),     \
-                                code_pair<NU>(l2, l2r), code_pair<NU>(h2, h2r)};    \
+        uint32_t af[4] = {code_pair<NU>(l1, l1r), code_pair<NU>(h1, h1r),           \
+                          code_pair<NU>(l2, l2r), code_pair<NU>(h2, h2r)};          \
+        if constexpr (A::kWin) for (uint32_t &x : af) x = code_up(x);               \
         mma16816(acc[NU], af, bv0, bv1);                                            \
     }
                     VSTEP(0) VSTEP(1) VSTEP(2) VSTEP(3) VSTEP(4) VSTEP(5) VSTEP(6) VSTEP(7)
@@ -1055,7 +1089,7 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
             float y[16];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float fi = (vunit ? pair_wo(i) : 1.f) * f;
+                const float fi = (vunit ? pair_wo(i) / vup : 1.f) * f;
                 y[i] = fmaf(acc[i][0] + acc[i][1], fi, pzf);       // channel 16g_ + i
                 y[8 + i] = fmaf(acc[i][2] + acc[i][3], fi, pzf);   // channel 16g_ + 8 + i
             }
@@ -1122,7 +1156,7 @@ template <bool kMass, class A>
 __global__ void __launch_bounds__(kThreads, 1) decode_dev_kernel(const __grid_constant__ A a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     launch_dependents();
-    if (!A::kPre) wait_prior_grid();   // the state table is written by the previous step
+    if (!follows_prefix_pass(a)) wait_prior_grid();   // the state table is written by the previous step
     const int tid = threadIdx.x;
     const int B = nseq(a);
     int *nq = dev_arr(a, 0), *rr = dev_arr(a, 1), *rs = dev_arr(a, 2), *ib = dev_arr(a, 3), *clo = dev_arr(a, 4);
@@ -1666,7 +1700,7 @@ int decode_launch(minikv_cache *c, const uint16_t *q, const uint16_t *k_new, con
     if (prefix) {   // every check has passed: the prefix pass goes first
         const int prc = prefix_launch(*prefix, c->B, q, Hq, sm_scale, stream, &tab);
         if (prc) return prc;
-        if (tab.P) pre = &tab;
+        pre = &tab;
     }
     Args a;
     a.k_codes = c->k_codes; a.v_codes = c->v_codes;

@@ -380,7 +380,8 @@ MINIKV_API int minikv_decode_attn_mass(minikv_cache *c, const uint16_t *q, const
  *         t <  n_sink       (the sinks).
  *       Every other token is left out of the softmax, whatever it holds, and is
  *       not read (up to the 32-token slices at the two ends of the hidden run).
- *       window >= n gives minikv_decode_attn's result.
+ *       window >= n attends to every token, as minikv_decode_attn (the same but
+ *       for rounding: this call's value sums are the more precise ones).
  *   Nothing is dropped from the cache: a hidden token stays stored, and a flush
  *   packs the oldest residual tokens as usual.
  *   Uniform, ragged and device-state caches; ws as for minikv_decode_attn (the

@@ -252,3 +252,35 @@ def test_a_prompt_and_steps_without_a_wait():
         _check_prefix(got[i], _expected(again, p, None, *y))
         mk.decode_attn(again, *y)
     _check_prompt(o, q, k, v, T, 0)
+
+
+@pytest.mark.parametrize("mode", ["uniform", "device"])
+def test_large_values(mode):
+    """Values up to fp16's limit and scores that grow along the cache: nothing overflows on the way."""
+    B, Hq, Hkv, n = 2, 8, 2, 3000
+    gen = torch.Generator(device=DEV).manual_seed(995)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=gen, device=DEV)
+
+    def load(n, B, cap):
+        c = mk.MiniKVCache(B, Hkv, cap, G=32, R=32, Hq=Hq)
+        k = (rand(B, Hkv, n, 128) * torch.linspace(0.2, 2, n, device=DEV)[:, None]).half()
+        v = (rand(B, Hkv, n, 128) * 15000).clamp(-65504, 65504).half()
+        if mode == "device" and B > 1:
+            c.set_device_state()
+            for b in range(B):
+                mk.quant_pack_seq(c, b, k[b], v[b])
+        else:
+            mk.quant_pack(c, k, v)
+        return c, k, v
+
+    x = rand(B, Hq, 128).half(), rand(B, Hkv, 128).half(), rand(B, Hkv, 128).half()
+    cache, k, v = load(n, B, n + 8)
+    ref = _window_ref(cache, *x, 2500, 4)
+    _check_step(mk.decode_attn_window(cache, *x, 2500, 4), ref)
+    cache, prefix = load(n, B, n + 8)[0], load(1500, 1, 1600)[0]
+    ref = _expected(cache, prefix, None, *x)
+    _check_prefix(mk.decode_attn_prefix(cache, prefix, *x), ref)
+    q = rand(B, Hq, n, 128).half()
+    _check_prompt(mk.window_prefill(q, k, v, 500, 4), q, k, v, 500, 4)
