@@ -118,60 +118,57 @@ __device__ __forceinline__ Blocks blocks_of(const Args &a, int p0, int p1) {
     return b;
 }
 
-// One query row from scratch over its visible keys (fp32, one thread a row): a
-// pass for the maximum and the sum, then 32 channels at a time.
-__device__ __forceinline__ void slow_row(const Args &a, size_t qrow, size_t kvplane, int p, unsigned char *dst, int sw) {
-    const uint4 *q = reinterpret_cast<const uint4 *>(a.q + qrow * kD);
-    const int lo = max(0, p - (a.window - 1));
-    float m = -INFINITY, l = 0.f;
+// One query row from scratch over its visible keys (fp32, a warp a row, a lane
+// four channels), eight keys at a time: the row at position p into its place in
+// the swizzled output tile, dst its first byte there.
+__device__ __forceinline__ void slow_row(const Args &a, size_t qrow, size_t kvplane, int p, unsigned char *dst, int sw,
+                                         int lane) {
+    constexpr int kKeys = 8;
+    const int lo = max(0, p - (a.window - 1)), ns = min(a.n_sink, lo), n = ns + p - lo + 1;
+    auto quad = [&](const uint16_t *row, float (&f)[4]) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(row) + lane);
+        const float2 x = unpack_half2(u.x), y = unpack_half2(u.y);
+        f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
+    };
+    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+    quad(a.q + qrow * kD, q);
 #pragma unroll 1
-    for (int pass = 0; pass < 5; ++pass) {
-        float o[32];
+    for (int t0 = 0; t0 < n; t0 += kKeys) {
+        float x[kKeys], v[kKeys][4], top = m;
 #pragma unroll
-        for (int d = 0; d < 32; ++d) o[d] = 0.f;
-#pragma unroll 1
-        for (int j = 0; j <= p; ++j) {
-            if (j < lo && j >= a.n_sink) j = lo;
-            const uint4 *kr = reinterpret_cast<const uint4 *>(a.k + (kvplane * a.Tk + j) * kD);
-            float x = 0.f;
-#pragma unroll 1
-            for (int c = 0; c < 16; ++c) {
-                float qa[8], ka[8];
-                h8_to_f(__ldg(q + c), qa);
-                h8_to_f(__ldg(kr + c), ka);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x = fmaf(qa[i], ka[i], x);
-            }
-            x *= a.scale_log2;
-            if (pass == 0) {
-                const float mn = fmaxf(m, x);
-                l = l * (m == mn ? 1.f : ex2(m - mn)) + (x == -INFINITY ? 0.f : ex2(x - mn));
-                m = mn;
-            } else {
-                const float e = x == -INFINITY ? 0.f : ex2(x - m);
-                const uint4 *vr = reinterpret_cast<const uint4 *>(a.v + (kvplane * a.Tk + j) * kD) + 4 * (pass - 1);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float va[8];
-                    h8_to_f(__ldg(vr + c), va);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[8 * c + i] = fmaf(e, va[i], o[8 * c + i]);
-                }
-            }
+        for (int i = 0; i < kKeys; ++i) {
+            const int t = min(t0 + i, n - 1);
+            const size_t j = kvplane * a.Tk + (t < ns ? t : lo + t - ns);
+            float k[4];
+            quad(a.k + j * kD, k);
+            quad(a.v + j * kD, v[i]);
+            x[i] = fmaf(q[3], k[3], fmaf(q[2], k[2], fmaf(q[1], k[1], q[0] * k[0])));
         }
-        if (pass == 0) continue;
-        const float inv = 1.f / l;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {   // as the epilogue writes it: 16-byte chunk ch of the row
-            const int ch = 4 * (pass - 1) + c;
-            uint4 u;
-            u.x = pack_half2(o[8 * c] * inv, o[8 * c + 1] * inv);
-            u.y = pack_half2(o[8 * c + 2] * inv, o[8 * c + 3] * inv);
-            u.z = pack_half2(o[8 * c + 4] * inv, o[8 * c + 5] * inv);
-            u.w = pack_half2(o[8 * c + 6] * inv, o[8 * c + 7] * inv);
-            *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kM * 128) + (((ch & 7) ^ sw) << 4)) = u;
+        for (int i = 0; i < kKeys; ++i) {
+#pragma unroll
+            for (int s = 16; s; s >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], s);
+            x[i] = t0 + i < n ? x[i] * a.scale_log2 : -INFINITY;
+            top = fmaxf(top, x[i]);
+        }
+        const float al = m == top ? 1.f : ex2(m - top);
+        m = top;
+        l *= al;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] *= al;
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            if (x[i] == -INFINITY) continue;   // (the same for the whole warp)
+            const float e = ex2(x[i] - m);
+            l += e;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[c] = fmaf(e, v[i][c], o[c]);
         }
     }
+    const float inv = 1.f / l;
+    const int ch = lane >> 1;   // as the epilogue writes it: 16-byte chunk ch of the row, in halves
+    *reinterpret_cast<uint2 *>(dst + (ch >> 3) * (kM * 128) + (((ch & 7) ^ sw) << 4) + 8 * (lane & 1)) =
+        make_uint2(pack_half2(o[0] * inv, o[1] * inv), pack_half2(o[2] * inv, o[3] * inv));
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -399,8 +396,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // (weights that are NaN themselves, or none at all, give NaN whatever the values are)
-            if ((bad & 0x80008000u) && l > 0.f && l < INFINITY && ti.q0 + r < a.Tq)
-                slow_row(a, ((size_t)b * a.Hq + ti.h) * a.Tq + ti.q0 + r, unit, p, qbytes + r * 128, r & 7);
+            uint32_t again = __ballot_sync(0xffffffffu, (bad & 0x80008000u) && l > 0.f && l < INFINITY && ti.q0 + r < a.Tq);
+            __syncwarp();   // the rows' lanes have written them
+            for (; again; again &= again - 1) {
+                const int ra = 32 * (warp & 3) + __ffs(again) - 1;
+                slow_row(a, ((size_t)b * a.Hq + ti.h) * a.Tq + ti.q0 + ra, unit, ti.p0 + ra, qbytes + ra * 128, ra & 7, lane);
+            }
             tc::fence_proxy_async_smem();
         }
         asm volatile("bar.sync %0, 128;\n" ::"r"(1 + t) : "memory");
@@ -425,9 +426,9 @@ int g_sms[kMaxDevices] = {};
 long long tiles_of(int Hq, int Hkv, int Tq) { return ((long long)Tq + kM - 1) / kM * (Hq / Hkv); }
 
 // Query tiles of a CTA: two share every K / V block they read and hide each
-// other's softmax (8192 tokens, window 4096: 442 us); one while there are SMs for
-// all of them, as a tile alone is done sooner (512 tokens, window 128: CTA of two
-// 16.5 us).
+// other's softmax (8192 tokens, window 4096: 430 us); one while there are SMs for
+// all of them, as a tile alone is done sooner (512 tokens, window 128, 4 heads:
+// 18.4 us with CTAs of two, 12.3 with one; 9.3 now).
 int tiles_per_cta(int B, int Hq, int Hkv, int Tq, int sms) {
     return (long long)B * Hkv * tiles_of(Hq, Hkv, Tq) <= sms ? 1 : 2;
 }

@@ -180,3 +180,16 @@ def test_nan_stays_with_the_rows_that_see_it():
     assert not torch.isfinite(o[0, 2:, seen, ch]).any()
     o[0, 2:, seen, ch] = clean[0, 2:, seen, ch]
     _check(o, q0, k, v0, window, n_sink)   # (rows that share a block with the value are computed again)
+
+
+@pytest.mark.parametrize("window,n_sink", [(70, 3), (2000, 0), (129, 200)])
+def test_rows_beside_padding_of_nan(window, n_sink):
+    """Prompts padded behind their ends with NaN: the rows before the padding, some beside it in a block, are right."""
+    T, end = 900, 777
+    q, k, v = _qkv(1, 6, 2, T, T, seed=902)
+    k0, v0 = k.clone(), v.clone()
+    for t in (k, v, q):
+        t[:, :, end:] = float("nan")
+    o = mk.window_prefill(q, k, v, window, n_sink)
+    q[:, :, end:] = 0
+    _check(o, q, k0, v0, window, n_sink, rows=slice(0, end))
