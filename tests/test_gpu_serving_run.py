@@ -284,3 +284,27 @@ def test_large_values(mode):
     _check_prefix(mk.decode_attn_prefix(cache, prefix, *x), ref)
     q = rand(B, Hq, n, 128).half()
     _check_prompt(mk.window_prefill(q, k, v, 500, 4), q, k, v, 500, 4)
+
+
+@pytest.mark.parametrize("n,shared", [(0, None), (300, [0, 0, 0])])
+def test_nobody_attends_to_the_prefix_captured(n, shared, deterministic):
+    """An empty prefix, or one that no sequence shares: steps queued without a wait, eager and replayed, are
+    decode_attn's."""
+    cache, other = (_batch([100, 40, 300], 8, 2, "device", steps=40) for _ in range(2))
+    prefix = _prefix(2, n) if n else mk.MiniKVCache(1, 2, 64, R=32)
+    x = [t.clone() for t in _inputs(3, 8, 2, 0, seed=996)]
+    out = torch.empty_like(x[0])
+    mk.decode_attn_prefix(cache, prefix, *x, shared=shared, out=out)
+    mk.decode_attn(other, *x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mk.decode_attn_prefix(cache, prefix, *x, shared=shared, out=out)
+        mk.decode_attn_prefix(cache, prefix, out, x[1], x[2], shared=shared, out=out)
+    for i in range(20):
+        for dst, src in zip(x, _inputs(3, 8, 2, i, seed=996)):
+            dst.copy_(src)
+        graph.replay()
+        ref = mk.decode_attn(other, mk.decode_attn(other, *x), x[1], x[2])
+        assert torch.equal(out, ref), i
+    assert [cache.seq_state(b) for b in range(3)] == [other.seq_state(b) for b in range(3)]
