@@ -2,7 +2,9 @@
 sharing sequence attends to the prefix cache's tokens and its own.
 
 Tolerance of an output value o = sum p v / sum p: half an fp16 step of o
-(2^-11 |o|), and for the prefix's tokens, whose operands are fp16:
+(2^-11 |o|), and for the prefix's tokens what fp16 operands of the two products
+would cost (the kernel's own key and value operands are exact, only P is
+rounded, so it has room to spare):
   * P and the dequantized value each rounded once, half a step each: 2^-10 mean,
     mean = sum p |v| / sum p; 2^-25 max |v| a token below fp16's normal range
     (against a sum of at least 1);
