@@ -193,3 +193,19 @@ def test_rows_beside_padding_of_nan(window, n_sink):
     o = mk.window_prefill(q, k, v, window, n_sink)
     q[:, :, end:] = 0
     _check(o, q, k0, v0, window, n_sink, rows=slice(0, end))
+
+
+@pytest.mark.parametrize("n_sink", [15, 16, 31, 32, 33, 127, 128, 129])
+@pytest.mark.parametrize("Hq,Hkv,Tq,Tk,window", [(2, 1, 600, 600, 64), (3, 1, 140, 1000, 200)])
+def test_sizes_of_the_sink_block(Hq, Hkv, Tq, Tk, window, n_sink):
+    """Sinks that take part of a block, a whole one or more; the rest of the block may hold anything."""
+    q, k, v = _qkv(1, Hq, Hkv, Tq, Tk, seed=903)
+    o = mk.window_prefill(q, k, v, window, n_sink)
+    _check(o, q, k, v, window, n_sink)
+    first = max(0, n_sink + window + 1 - (Tk - Tq))   # rows from here on see nothing between the sinks and n_sink + 1
+    k[:, :, n_sink:n_sink + 1] = float("nan")
+    v[:, :, n_sink:n_sink + 1] = float("nan")
+    bad = mk.window_prefill(q, k, v, window, n_sink)
+    k[:, :, n_sink:n_sink + 1] = 0
+    v[:, :, n_sink:n_sink + 1] = 0
+    _check(bad, q, k, v, window, n_sink, rows=slice(first, Tq))
