@@ -105,11 +105,14 @@ def _dev(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     return t.data_ptr()
 
 
-# torch's raw handle of the current stream, without building a Stream object (2 us a call)
+# torch's raw handles, without building Stream or device objects (2 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 _cuda_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_F16 = torch.float16
+
+
+def _current_stream(device: int) -> int:
+    return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _stream(stream, device) -> int:
@@ -119,20 +122,22 @@ def _stream(stream, device) -> int:
     return s.cuda_stream
 
 
-def _elsewhere(stream, t: torch.Tensor, *others: torch.Tensor):
-    """None where a call on `t` and `others` may run as things are.  Else what to
-    run it under: their device made current (the library launches on the current
-    one), and `stream`, so that what the call allocates belongs to the stream it
-    runs on."""
-    d = t.get_device()
-    for x in others:
-        if x.get_device() != d:
-            raise ValueError(f"tensors on {t.device} and {x.device}")
-    if stream is None and (d < 0 or d == _cuda_device()):
-        return None
+def _at(t: torch.Tensor, dtype: torch.dtype, device: int, name: str) -> int:
+    """_dev of a tensor that has to be on the given device."""
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{device}")
+
+
+def _elsewhere(stream, device: int):
+    """What a call on tensors of another device than the current one, or on another
+    stream, runs under: their device made current (the library launches on the
+    current one), and the stream, so that what the call allocates belongs to it."""
+    if device < 0:
+        raise TypeError("q must be a CUDA tensor")
     under = contextlib.ExitStack()
-    if d >= 0:
-        under.enter_context(torch.cuda.device(d))
+    under.enter_context(torch.cuda.device(device))
     if stream is not None:
         under.enter_context(torch.cuda.stream(stream))
     return under
@@ -144,8 +149,9 @@ def _check_step(cache, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     B, Hq, D = shape
     if B != c.B or D != c.D:
         raise ValueError(f"q {tuple(shape)} does not match a cache of B={c.B}, D={c.D}")
-    if k_new.shape != (B, c.Hkv, D) or v_new.shape != k_new.shape:
-        raise ValueError(f"k_new {tuple(k_new.shape)}, v_new {tuple(v_new.shape)}: both must be {(B, c.Hkv, D)}")
+    new = (B, c.Hkv, D)
+    if k_new.shape != new or v_new.shape != new:
+        raise ValueError(f"k_new {tuple(k_new.shape)}, v_new {tuple(v_new.shape)}: both must be {new}")
     if out is not None and out.shape != shape:
         raise ValueError(f"out {tuple(out.shape)} does not match q {tuple(shape)}")
     return shape
@@ -352,9 +358,9 @@ def window_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: in
         sm_scale = 1.0 / math.sqrt(D)
     if o is not None and o.shape != q.shape:
         raise ValueError(f"o {tuple(o.shape)} does not match q {tuple(q.shape)}")
-    under = _elsewhere(stream, q, k, v)
-    if under is not None:
-        with under:
+    d = q.get_device()
+    if stream is not None or d < 0 or d != _cuda_device():
+        with _elsewhere(stream, d):
             return window_prefill(q, k, v, window, n_sink, sm_scale, o, ws, None, library)
     if o is None:
         o = torch.empty_like(q)
@@ -362,9 +368,8 @@ def window_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: in
         ws = torch.empty(max(workspace_size(OP_WINDOW_PREFILL, B, Hq, Hkv, Tq, D), 256), dtype=torch.uint8,
                          device=q.device)
     _check((library or lib()).minikv_window_prefill(
-        _dev(q, torch.float16, "q"), _dev(k, torch.float16, "k"), _dev(v, torch.float16, "v"), B, Hq, Hkv, Tq, Tk, D,
-        int(window), int(n_sink), float(sm_scale), _dev(o, torch.float16, "o"), _dev(ws, torch.uint8, "ws"), ws.numel(),
-        _stream(None, q.device)))
+        _at(q, _F16, d, "q"), _at(k, _F16, d, "k"), _at(v, _F16, d, "v"), B, Hq, Hkv, Tq, Tk, D, int(window), int(n_sink),
+        float(sm_scale), _at(o, _F16, d, "o"), _at(ws, torch.uint8, d, "ws"), ws.numel(), _current_stream(d)))
     return o
 
 
@@ -460,9 +465,9 @@ def decode_attn_window(cache: MiniKVCache, q: torch.Tensor, k_new: torch.Tensor,
     included) and the first `n_sink` of each sequence, in order of arrival."""
     if ws is None:
         ws = cache.ws
-    under = _elsewhere(stream, q, k_new, v_new, ws)
-    if under is not None:
-        with under:
+    d = q.get_device()
+    if stream is not None or d < 0 or d != _cuda_device():
+        with _elsewhere(stream, d):
             return decode_attn_window(cache, q, k_new, v_new, window, n_sink, sm_scale, out, ws)
     B, Hq, D = _check_step(cache, q, k_new, v_new, out)
     if sm_scale is None:
@@ -470,9 +475,9 @@ def decode_attn_window(cache: MiniKVCache, q: torch.Tensor, k_new: torch.Tensor,
     if out is None:
         out = torch.empty_like(q)
     _check(lib().minikv_decode_attn_window(
-        ctypes.byref(cache.c), _dev(q, torch.float16, "q"), _dev(k_new, torch.float16, "k_new"),
-        _dev(v_new, torch.float16, "v_new"), Hq, int(window), int(n_sink), float(sm_scale),
-        _dev(out, torch.float16, "out"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(None, q.device)))
+        ctypes.byref(cache.c), _at(q, _F16, d, "q"), _at(k_new, _F16, d, "k_new"), _at(v_new, _F16, d, "v_new"), Hq,
+        int(window), int(n_sink), float(sm_scale), _at(out, _F16, d, "out"), _at(ws, torch.uint8, d, "ws"), ws.numel(),
+        _current_stream(d)))
     return out
 
 
@@ -489,9 +494,9 @@ def decode_attn_prefix(cache: MiniKVCache, prefix: MiniKVCache, q: torch.Tensor,
     also attend to every token of `prefix`, a cache of one sequence.  The default
     workspace is made once per cache, zero-filled, and kept on it (not while a
     graph is captured: the graph would own it)."""
-    under = _elsewhere(stream, q, k_new, v_new)
-    if under is not None:
-        with under:
+    d = q.get_device()
+    if stream is not None or d < 0 or d != _cuda_device():
+        with _elsewhere(stream, d):
             return decode_attn_prefix(cache, prefix, q, k_new, v_new, shared, sm_scale, out, ws, None, library)
     B, Hq, D = _check_step(cache, q, k_new, v_new, out)
     if sm_scale is None:
@@ -512,9 +517,9 @@ def decode_attn_prefix(cache: MiniKVCache, prefix: MiniKVCache, q: torch.Tensor,
             cache.ws_prefix = torch.zeros(need, dtype=torch.uint8, device=cache.device)
         ws = cache.ws_prefix
     _check((library or lib()).minikv_decode_attn_prefix(
-        ctypes.byref(cache.c), ctypes.byref(prefix.c), shared, _dev(q, torch.float16, "q"),
-        _dev(k_new, torch.float16, "k_new"), _dev(v_new, torch.float16, "v_new"), Hq, float(sm_scale),
-        _dev(out, torch.float16, "out"), _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(None, q.device)))
+        ctypes.byref(cache.c), ctypes.byref(prefix.c), shared, _at(q, _F16, d, "q"), _at(k_new, _F16, d, "k_new"),
+        _at(v_new, _F16, d, "v_new"), Hq, float(sm_scale), _at(out, _F16, d, "out"), _at(ws, torch.uint8, d, "ws"),
+        ws.numel(), _current_stream(d)))
     return out
 
 

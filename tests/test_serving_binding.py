@@ -30,19 +30,29 @@ def test_step_shape_refusals(change):
         _step(**change)
 
 
-def test_tensors_of_two_devices_are_refused():
-    with pytest.raises(ValueError, match="tensors on"):
-        mk._elsewhere(None, torch.empty(1), torch.empty(1), torch.empty(1, device="cuda") if torch.cuda.is_available()
-                      else _Fake())
-    assert mk._elsewhere(None, torch.empty(1), torch.empty(1)) is None
-
-
-class _Fake:
-    """A tensor of device 1."""
+class _Fake(torch.Tensor):
+    """A tensor that says it is on CUDA device 1."""
     is_cuda, device = True, "cuda:1"
 
     def get_device(self):
         return 1
+
+
+def test_tensors_of_two_devices_are_refused():
+    t = torch.empty(4, dtype=torch.float16).as_subclass(_Fake)
+    assert mk._at(t, torch.float16, 1, "k") == t.data_ptr()
+    with pytest.raises(ValueError, match="k is on cuda:1, other tensors on cuda:0"):
+        mk._at(t, torch.float16, 0, "k")
+    with pytest.raises(TypeError, match="k must be torch.float16"):
+        mk._at(t.float(), torch.float16, 1, "k")
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        mk._at(torch.empty(4, dtype=torch.float16), torch.float16, 0, "k")
+
+
+def test_tensors_of_the_cpu_are_refused():
+    q, k = torch.empty((1, 4, 9, 128), dtype=torch.float16), torch.empty((1, 2, 9, 128), dtype=torch.float16)
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        mk.window_prefill(q, k, k, 4)
 
 
 @pytest.mark.parametrize("q,k,v,o", [
