@@ -469,18 +469,21 @@ __host__ __device__ constexpr int pair_pos(int i) { return i < 5 ? 2 * i : 2 * (
 // does) and 2^(24 - pos) (value output scale)
 __host__ __device__ constexpr float pair_wq(int i) { return 1.f / (float)(1 << pair_pos(i)); }
 __host__ __device__ constexpr float pair_wo(int i) { return (float)(1 << (24 - pair_pos(i))); }
-// Windowed calls take the value codes through one product with 2^10, which makes
-// normal numbers of them.  The tensor cores align a sum by the operands' exponent
-// fields, and a subnormal's says 2^-14 whatever its leading zeros are: sums over
-// thousands of tokens come out short by some 1e-4 of the (large, positive) sum of
-// p c, which the zero points then cancel.  Error against 64 bits, relative to the
-// output: 3.6e-4 without, 2.1e-4 (the output's own rounding) with it at 4100
-// visible tokens; 24.5 -> 25.5 us there, 152.6 -> 154.0 for 48 sequences without
-// grouping.  (The same for the key codes changes nothing: short sums of both signs.)
+// Windowed calls, and the sequences behind a shared prefix that share it, take the
+// value codes through one product with 2^10, which makes normal numbers of them.
+// The tensor cores align a sum by the operands' exponent fields, and a subnormal's
+// says 2^-14 whatever its leading zeros are: sums over thousands of tokens come out
+// short by some 1e-4 of the (large, positive) sum of p c, which the zero points then
+// cancel.  Error against 64 bits, relative to the output: 3.6e-4 without, 2.1e-4 (the
+// output's own rounding) with it at 4100 visible tokens; 24.5 -> 25.5 us there, 152.6
+// -> 154.0 for 48 sequences without grouping.  (The same for the key codes changes
+// nothing: short sums of both signs.)  A sequence that does not share the prefix is
+// summed as by minikv_decode_attn, bit for bit: its codes are multiplied by 1.
 constexpr float kCodeUp = 1024.f;
-__device__ __forceinline__ uint32_t code_up(uint32_t x) {
+constexpr uint32_t kCodeUp2 = 0x64006400u, kCodeAsIs2 = 0x3C003C00u;   // fp16x2 1024 and 1
+__device__ __forceinline__ uint32_t code_up(uint32_t x, uint32_t by) {
     uint32_t y;
-    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(x), "r"(0x64006400u));
+    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(x), "r"(by));
     return y;
 }
 constexpr float kScoreUnit = 16777216.f;   // packed scores come out as code q s 2^-24
@@ -566,7 +569,7 @@ __device__ void finish_unit(const A &a, Smem &sm, const Seg &s, const WinSeq &w,
     if constexpr (A::kPre) {
         // the row's states over the shared prefix, from the pass before this kernel
         const PreTab &t = a.pre;
-        const int place = t.P == 0 ? -1 : t.listed ? t.place[b] : b;
+        const int place = prefix_place(t, b);
         if (place >= 0) wait_prior_grid();   // the prefix pass (this kernel did not wait for it at its start)
         if (place >= 0 && h < a.g) {
             const int row = place * a.g + h, pu = (row >> t.lgN) * a.Hkv + kvh, n = row & ((1 << t.lgN) - 1);
@@ -818,7 +821,10 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
         float m_ref = -INFINITY, l = 0.f, pz = 0.f;
-        constexpr float vup = A::kWin ? kCodeUp : 1.f;
+        float vup = A::kWin ? kCodeUp : 1.f;   // factor of the value codes
+        if constexpr (A::kPre) vup = prefix_place(a.pre, sg.b) >= 0 ? kCodeUp : 1.f;
+        const float vdn = vup == 1.f ? 1.f : 1.f / kCodeUp;
+        const uint32_t vup2 = vup == 1.f ? kCodeAsIs2 : kCodeUp2;
         bool vunit = false;   // acc holds packed-value units (x 2^(pos-24) vup) once a packed item was seen
         uint32_t qb = 0;      // this segment's q buffer (shared address)
 
@@ -1069,7 +1075,7 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
     {                                                                               \
         uint32_t af[4] = {code_pair<NU>(l1, l1r), code_pair<NU>(h1, h1r),           \
                           code_pair<NU>(l2, l2r), code_pair<NU>(h2, h2r)};          \
-        if constexpr (A::kWin) for (uint32_t &x : af) x = code_up(x);               \
+        if constexpr (A::kWin || A::kPre) for (uint32_t &x : af) x = code_up(x, vup2); \
         mma16816(acc[NU], af, bv0, bv1);                                            \
     }
                     VSTEP(0) VSTEP(1) VSTEP(2) VSTEP(3) VSTEP(4) VSTEP(5) VSTEP(6) VSTEP(7)
@@ -1097,7 +1103,7 @@ __device__ void run_cta(const A &a, Smem &sm, int c) {
             float y[16];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float fi = (vunit ? pair_wo(i) / vup : 1.f) * f;
+                const float fi = (vunit ? pair_wo(i) * vdn : 1.f) * f;
                 y[i] = fmaf(acc[i][0] + acc[i][1], fi, pzf);       // channel 16g_ + i
                 y[8 + i] = fmaf(acc[i][2] + acc[i][3], fi, pzf);   // channel 16g_ + 8 + i
             }

@@ -19,6 +19,10 @@ struct PreTab {
     int listed;          // 1: place[b] holds, 0: every sequence shares
     short place[MINIKV_MAX_RAGGED_SEQS];   // -1: sequence b does not share
 };
+// sequence b's place among the sharing ones, -1: it attends to nothing of the prefix
+__device__ __forceinline__ int prefix_place(const PreTab &t, int b) {
+    return t.P == 0 ? -1 : t.listed ? t.place[b] : b;
+}
 // the CTA whose range [c T / P, (c + 1) T / P) holds tile x
 __host__ __device__ __forceinline__ int pre_cta(const PreTab &t, int x) {
     return (int)((((unsigned long long)x + 1) * (unsigned)t.P - 1) / (unsigned)t.T);
