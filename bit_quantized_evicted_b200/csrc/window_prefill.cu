@@ -240,11 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 issued = 2 * j + 2;
             }
-            if (*reinterpret_cast<volatile int *>(&s.abort)) {   // let the loads queued here land before the CTA exits
-                mbar_wait(&s.q_full, 0);
-                for (int e = issued > kRing ? issued - kRing : 0; e < issued; ++e)
-                    mbar_wait(&s.full[e % kRing], (e / kRing) & 1);
-            }
+            // Every load queued here lands before the CTA exits, whoever gave up and whenever: another role may abort
+            // after any look at s.abort.  (Without an abort these phases are long over, or about to be.)
+            mbar_wait(&s.q_full, 0);
+            for (int e = issued > kRing ? issued - kRing : 0; e < issued; ++e)
+                mbar_wait(&s.full[e % kRing], (e / kRing) & 1);
         } else if (warp == 2 || (warp == 3 && two)) {
             // ---------------- MMA issuer of tile t (the warp waits together, one lane issues)
             const int t = warp - 2;
