@@ -180,13 +180,12 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 tc::tma_load_3d(s.k[ks][1], &map_k, 64, j * kTileN, kvh, &s.k_full[ks]);
                 issued = j + 1;
             }
-            if (*reinterpret_cast<volatile int *>(&s.abort)) {
-                // a wait gave up: let the loads this thread queued land before the CTA exits
-                // (each stage holds at most one unconsumed load; waits on a finished phase return at once)
-                mbar_wait(&s.q_full, 0);
-                for (int j = issued > kKStages ? issued - kKStages : 0; j < issued; ++j)
-                    mbar_wait(&s.k_full[j % kKStages], (j / kKStages) & 1);
-            }
+            // Every load queued here lands before the CTA exits, whoever gave up and whenever: another role may abort
+            // after any look at s.abort.  (Each stage holds at most one unconsumed load; waits on a finished phase
+            // return at once.)
+            mbar_wait(&s.q_full, 0);
+            for (int j = issued > kKStages ? issued - kKStages : 0; j < issued; ++j)
+                mbar_wait(&s.k_full[j % kKStages], (j / kKStages) & 1);
         }
         __syncwarp();
     } else if (warp == 2) {
@@ -201,9 +200,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 tc::tma_load_3d(s.v[vs][1], &map_v, 64, j * kTileN, kvh, &s.v_full[vs]);
                 issued = j + 1;
             }
-            if (*reinterpret_cast<volatile int *>(&s.abort))
-                for (int j = issued > kVStages ? issued - kVStages : 0; j < issued; ++j)
-                    mbar_wait(&s.v_full[j % kVStages], (j / kVStages) & 1);
+            for (int j = issued > kVStages ? issued - kVStages : 0; j < issued; ++j)   // as the K producer
+                mbar_wait(&s.v_full[j % kVStages], (j / kVStages) & 1);
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -47,3 +47,21 @@ def test_short_window_prompts(probe, B, Hq, Hkv, T, window, n_sink):
         assert torch.equal(mk.window_prefill(q, k, v, window, n_sink, ws=ws), ref)
         assert mk.window_prefill_status(ws, B, Hq, Hkv, T) == 0
     _check(ref[:1], q[:1], k[:1], v[:1], window, n_sink)
+
+
+@pytest.mark.parametrize("B,H,T", [(1, 2, 100), (40, 4, 128), (8, 4, 256), (4, 8, 384)])
+def test_short_prompts(probe, B, H, T):
+    q, k, v = _qkv(B, H, H, T, T, seed=931)
+    W = 16
+    ws = torch.zeros(mk.workspace_size(mk.OP_SELECT_PREFILL, B, H, H, T, 128, W), dtype=torch.uint8, device=DEV)
+    ref, scores = mk.select_prefill(q, k, v, W, ws=ws)
+    o, sc = torch.empty_like(ref), torch.empty_like(scores)
+    for _ in range(10):
+        assert probe.minikv_select_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, H, T, 128, W, 128 ** -0.5,
+                                           o.data_ptr(), sc.data_ptr(), ws.data_ptr(), ws.numel(),
+                                           torch.cuda.current_stream().cuda_stream) == mk.OK
+        assert mk.select_prefill_status(ws, B, H, W, library=probe) == 1
+        again = mk.select_prefill(q, k, v, W, ws=ws)
+        assert torch.equal(again[0], ref) and torch.equal(again[1], scores)
+        assert mk.select_prefill_status(ws, B, H, W) == 0
+    _check(ref[:1], q[:1], k[:1], v[:1], T, 0)
