@@ -130,6 +130,12 @@ def _at(t: torch.Tensor, dtype: torch.dtype, device: int, name: str) -> int:
     raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{device}")
 
 
+def _cache_at(cache, device: int, name: str) -> None:
+    """Refuse a cache that is not on the device of the call's tensors (a CPU tensor is refused where it is looked at)."""
+    if device >= 0 and cache.device.index != device:
+        raise ValueError(f"{name} is on {cache.device}, other tensors on cuda:{device}")
+
+
 def _elsewhere(stream, device: int):
     """What a call on tensors of another device than the current one, or on another
     stream, runs under: their device made current (the library launches on the
@@ -466,6 +472,7 @@ def decode_attn_window(cache: MiniKVCache, q: torch.Tensor, k_new: torch.Tensor,
     if ws is None:
         ws = cache.ws
     d = q.get_device()
+    _cache_at(cache, d, "cache")
     if stream is not None or d < 0 or d != _cuda_device():
         with _elsewhere(stream, d):
             return decode_attn_window(cache, q, k_new, v_new, window, n_sink, sm_scale, out, ws)
@@ -495,6 +502,8 @@ def decode_attn_prefix(cache: MiniKVCache, prefix: MiniKVCache, q: torch.Tensor,
     workspace is made once per cache, zero-filled, and kept on it (not while a
     graph is captured: the graph would own it)."""
     d = q.get_device()
+    _cache_at(cache, d, "cache")
+    _cache_at(prefix, d, "prefix")
     if stream is not None or d < 0 or d != _cuda_device():
         with _elsewhere(stream, d):
             return decode_attn_prefix(cache, prefix, q, k_new, v_new, shared, sm_scale, out, ws, None, library)
