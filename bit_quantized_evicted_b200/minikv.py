@@ -142,6 +142,8 @@ def _elsewhere(stream, device: int):
     current one), and the stream, so that what the call allocates belongs to it."""
     if device < 0:
         raise TypeError("q must be a CUDA tensor")
+    if stream is not None and stream.device.index != device:   # (it would be entered in place of the tensors' device)
+        raise ValueError(f"stream is on {stream.device}, tensors on cuda:{device}")
     under = contextlib.ExitStack()
     under.enter_context(torch.cuda.device(device))
     if stream is not None:

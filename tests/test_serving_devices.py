@@ -1,5 +1,5 @@
-"""Caches of another GPU than the call's tensors: refused by the binding before
-the library sees a pointer.  On the CPU, with stand-ins."""
+"""Caches and streams of another GPU than the call's tensors: refused by the
+binding before the library sees a pointer.  On the CPU, with stand-ins."""
 from types import SimpleNamespace
 
 import pytest
@@ -48,3 +48,14 @@ def test_prefix_step_on_caches_of_another_device(step, cache, prefix, match):
     for ws in (None, _fake(64)):
         with pytest.raises(ValueError, match=match):
             mk.decode_attn_prefix(_cache(cache), _cache(prefix, 1), *step, ws=ws, library=_NoLibrary())
+
+
+def test_streams_of_another_device(step):
+    stream = SimpleNamespace(device=torch.device("cuda", 0), cuda_stream=7)
+    q, kn, vn = step
+    k = _fake(2, 2, 9, 128)
+    for call in (lambda: mk.decode_attn_window(_cache(1), *step, 8, stream=stream),
+                 lambda: mk.decode_attn_prefix(_cache(1), _cache(1, 1), *step, stream=stream, library=_NoLibrary()),
+                 lambda: mk.window_prefill(_fake(2, 8, 9, 128), k, k, 4, stream=stream, library=_NoLibrary())):
+        with pytest.raises(ValueError, match="stream is on cuda:0, tensors on cuda:1"):
+            call()
