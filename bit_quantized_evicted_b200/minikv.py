@@ -136,6 +136,11 @@ def _cache_at(cache, device: int, name: str) -> None:
         raise ValueError(f"{name} is on {cache.device}, other tensors on cuda:{device}")
 
 
+def _count(n) -> int:
+    """A window or a number of sinks as the library's int: ctypes would drop the bits past 32, and with them the order."""
+    return max(-1, min(int(n), 0x7FFFFFFF))
+
+
 def _elsewhere(stream, device: int):
     """What a call on tensors of another device than the current one, or on another
     stream, runs under: their device made current (the library launches on the
@@ -376,7 +381,7 @@ def window_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: in
         ws = torch.empty(max(workspace_size(OP_WINDOW_PREFILL, B, Hq, Hkv, Tq, D), 256), dtype=torch.uint8,
                          device=q.device)
     _check((library or lib()).minikv_window_prefill(
-        _at(q, _F16, d, "q"), _at(k, _F16, d, "k"), _at(v, _F16, d, "v"), B, Hq, Hkv, Tq, Tk, D, int(window), int(n_sink),
+        _at(q, _F16, d, "q"), _at(k, _F16, d, "k"), _at(v, _F16, d, "v"), B, Hq, Hkv, Tq, Tk, D, _count(window), _count(n_sink),
         float(sm_scale), _at(o, _F16, d, "o"), _at(ws, torch.uint8, d, "ws"), ws.numel(), _current_stream(d)))
     return o
 
@@ -485,7 +490,7 @@ def decode_attn_window(cache: MiniKVCache, q: torch.Tensor, k_new: torch.Tensor,
         out = torch.empty_like(q)
     _check(lib().minikv_decode_attn_window(
         ctypes.byref(cache.c), _at(q, _F16, d, "q"), _at(k_new, _F16, d, "k_new"), _at(v_new, _F16, d, "v_new"), Hq,
-        int(window), int(n_sink), float(sm_scale), _at(out, _F16, d, "out"), _at(ws, torch.uint8, d, "ws"), ws.numel(),
+        _count(window), _count(n_sink), float(sm_scale), _at(out, _F16, d, "out"), _at(ws, torch.uint8, d, "ws"), ws.numel(),
         _current_stream(d)))
     return out
 
