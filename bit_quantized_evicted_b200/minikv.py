@@ -141,6 +141,20 @@ def _count(n) -> int:
     return max(-1, min(int(n), 0x7FFFFFFF))
 
 
+def _has_ws(cache, name: str, need: int) -> bool:
+    ws = getattr(cache, name, None)
+    return ws is not None and ws.numel() >= need
+
+
+def _own_ws(cache, name: str, need: int) -> torch.Tensor:
+    """A call's default workspace, zero-filled when made and kept on the cache.  One that is too small for a later
+    call (more query heads) is replaced but stays alive: a captured graph may have been given it."""
+    if not _has_ws(cache, name, need):
+        cache.ws_replaced = [*getattr(cache, "ws_replaced", ()), getattr(cache, name, None)]
+        setattr(cache, name, torch.zeros(need, dtype=torch.uint8, device=cache.device))
+    return getattr(cache, name)
+
+
 def _elsewhere(stream, device: int):
     """What a call on tensors of another device than the current one, or on another
     stream, runs under: their device made current (the library launches on the
@@ -461,9 +475,7 @@ def decode_attn_mass(cache: MiniKVCache, q: torch.Tensor, k_new: torch.Tensor, v
         raise ValueError(f"mass shape {tuple(mass.shape)}: expected {(cache.B, cache.Hkv, cache.cap + cache.R + cache.G)}")
     if ws is None:
         need = workspace_size(OP_DECODE_ATTN_MASS, B, Hq, cache.Hkv, cache.cap + cache.R + cache.G, D)
-        if getattr(cache, "ws_mass", None) is None or cache.ws_mass.numel() < need:
-            cache.ws_mass = torch.zeros(need, dtype=torch.uint8, device=cache.device)
-        ws = cache.ws_mass
+        ws = _own_ws(cache, "ws_mass", need)
     _check(lib().minikv_decode_attn_mass(
         ctypes.byref(cache.c), _dev(q, torch.float16, "q"), _dev(k_new, torch.float16, "k_new"),
         _dev(v_new, torch.float16, "v_new"), Hq, float(sm_scale), _dev(out, torch.float16, "out"),
@@ -526,12 +538,10 @@ def decode_attn_prefix(cache: MiniKVCache, prefix: MiniKVCache, q: torch.Tensor,
             shared = shared_rows(shared)
     if ws is None:
         need = workspace_size(OP_DECODE_ATTN_PREFIX, B, Hq, cache.Hkv, cache.cap + cache.R + cache.G, D)
-        if getattr(cache, "ws_prefix", None) is None or cache.ws_prefix.numel() < need:
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("decode_attn_prefix: the first call on a cache makes its workspace, which a captured "
-                                   "call cannot; pass ws or make a call before the capture")
-            cache.ws_prefix = torch.zeros(need, dtype=torch.uint8, device=cache.device)
-        ws = cache.ws_prefix
+        if not _has_ws(cache, "ws_prefix", need) and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("decode_attn_prefix: the first call on a cache makes its workspace, which a captured "
+                               "call cannot; pass ws or make a call before the capture")
+        ws = _own_ws(cache, "ws_prefix", need)
     _check((library or lib()).minikv_decode_attn_prefix(
         ctypes.byref(cache.c), ctypes.byref(prefix.c), shared, _at(q, _F16, d, "q"), _at(k_new, _F16, d, "k_new"),
         _at(v_new, _F16, d, "v_new"), Hq, float(sm_scale), _at(out, _F16, d, "out"), _at(ws, torch.uint8, d, "ws"),
