@@ -1494,8 +1494,9 @@ long long slowest_cta(const Shape &s, const Plan &p, long long stop) {
 // host thread, keyed by the bucketed state, saves the search.
 int choose_wu(const Shape &s, int sms, bool uniform, int ring) {
     std::vector<int> key;
-    key.reserve(5 + 2 * s.B);
+    key.reserve(6 + 2 * s.B);
     key.push_back(sms);
+    key.push_back(ring);   // (the bucketed residual counts stop at it)
     key.push_back(s.Hkv);
     key.push_back(s.B);
     key.push_back(uniform ? 1 : 0);
