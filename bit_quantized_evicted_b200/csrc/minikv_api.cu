@@ -51,6 +51,12 @@ int decode_plan_info(const minikv_cache *c, int *ctas, int *wu, int *first, int 
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// do two arrays of rows of kD fp16 share memory?
+static bool overlap(const uint16_t *a, size_t a_rows, const uint16_t *b, size_t b_rows) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return pa < pb + b_rows * kD * 2 && pb < pa + a_rows * kD * 2;
+}
+
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // shape rules shared by the cache-level calls
@@ -306,7 +312,11 @@ int minikv_window_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *
     const size_t need = window_prefill_workspace_bytes(B, Hq, Hkv, Tq);
     if (ws_bytes < need)
         return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: workspace of %zu bytes needed, %zu given", need, ws_bytes);
-    if (o == k || o == v) return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: o lies over k or v");
+    const size_t rows = (size_t)B * Hq * Tq, keys = (size_t)B * Hkv * Tk;
+    if (overlap(o, rows, k, keys) || overlap(o, rows, v, keys))
+        return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: o lies over k or v");
+    if (o != q && overlap(o, rows, q, rows))
+        return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: o lies over part of q (q itself may be given)");
     return window_prefill_launch(q, k, v, B, Hq, Hkv, Tq, Tk, window, n_sink, sm_scale, o, ws,
                                  static_cast<cudaStream_t>(stream));
 }

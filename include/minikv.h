@@ -235,8 +235,8 @@ MINIKV_API int minikv_select_prefill_status(const void *ws, size_t ws_bytes, int
  *   ws: device scratch of minikv_workspace_size(MINIKV_OP_WINDOW_PREFILL, B, Hq,
  *       Hkv, Tq, D, 0) bytes, no initial contents required; it holds the call's
  *       status words (minikv_window_prefill_status).
- * Errors: INVALID_ARG (null, misaligned, o at k or v, Tq > Tk, Hq % Hkv, window
- * < 1, n_sink < 0, sm_scale <= 0, ws too small), UNSUPPORTED (D != 128, B*Hq above
+ * Errors: INVALID_ARG (null, misaligned, o over k, v or part of q, Tq > Tk, Hq %
+ * Hkv, window < 1, n_sink < 0, sm_scale <= 0, ws too small), UNSUPPORTED (D != 128, B*Hq above
  * 65535, Tk above 2^30), CUDA (tensor-map encoding or launch failed).
  */
 MINIKV_API int minikv_window_prefill(const uint16_t *q, const uint16_t *k, const uint16_t *v, int B, int Hq, int Hkv,
