@@ -230,6 +230,8 @@ MINIKV_API int minikv_select_prefill_status(const void *ws, size_t ws_bytes, int
  *   window >= 1, n_sink >= 0; window >= Tk is causal attention over all keys.
  *   A key outside a row's set takes no part in that row, whatever it holds (an
  *   infinity or NaN among the values costs time, never another row's result).
+ *   A visible value that is not finite makes its channel what the sum gives, NaN
+ *   or the infinity.
  *   Key blocks no row sees are not read.
  *   sm_scale > 0 (the usual 1/sqrt(D)).
  *   ws: device scratch of minikv_workspace_size(MINIKV_OP_WINDOW_PREFILL, B, Hq,
