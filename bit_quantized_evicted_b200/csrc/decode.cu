@@ -25,7 +25,7 @@
 // Packed-item math (per warp, 32 tokens = 2 m-tiles of 16, g <= 4 heads):
 //   codes -> fp16 SUBNORMALS: one AND puts a 2-bit code at mantissa bit p of
 //     both halves of a 32-bit word (value code * 2^(p-24); the tensor cores
-//     take fp16 subnormals exactly);
+//     take them as they are, but long sums of them lose bits: see kCodeUp);
 //   scores S[tok, n] = sum_c code_c 2^(p_c-24) b_c over mma.sync.m16n8k16, with
 //     the 8 B columns interleaved per head: column 2h holds the fp16 "hi" part
 //     of q_h,c s_c 2^-p_c, column 2h+1 the exact remainder ("lo"), so the lane
@@ -284,7 +284,10 @@ struct ArgsDevWin : ArgsDev {
 // ---- a batch behind a shared prefix: each mode's arguments with the prefix pass's partials.  Such a launch follows
 // the prefix pass, which lets it start once all that came before is done: it waits for the pass itself only before
 // it merges the pass's states (at least one unit does: else the pass is not run, P = 0, and the launch waits at its
-// start like the others).
+// start like the others).  What orders the rest without a wait of its own: the pass lets its dependents go only after
+// its own wait, so all work before the pass is complete when this launch starts; and what that work wrote (state,
+// codes, ring, queries) is read here past L1 (cp.async.cg, __ldcg), or behind the acquire of a unit's counter or a
+// block barrier (the flush).  A load that L1 may serve in their place would need a wait of its own.
 struct ArgsUniPre : ArgsUni {
     static constexpr bool kPre = true;
     PreTab pre;

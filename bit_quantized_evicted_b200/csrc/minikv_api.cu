@@ -288,7 +288,7 @@ static int check_window_shape(int B, int Hq, int Hkv, int Tq) {
         return fail(MINIKV_ERR_INVALID_ARG, "window_prefill: B=%d Hq=%d Hkv=%d Tq=%d", B, Hq, Hkv, Tq);
     if ((size_t)B * Hq > 65535) return fail(MINIKV_ERR_UNSUPPORTED, "window_prefill: B*Hq above 65535");
     if (window_prefill_status_words(B, Hq, Hkv, Tq) > 0x7fffffff)
-        return fail(MINIKV_ERR_UNSUPPORTED, "window_prefill: more than 2^31 pairs of query tiles");
+        return fail(MINIKV_ERR_UNSUPPORTED, "window_prefill: more than 2^31 query tiles");
     return MINIKV_OK;
 }
 

@@ -11,7 +11,9 @@
 //
 // Exact operands.  A dequantized c s + z needs more than fp16's 11 bits, but
 // (c - o) s / 2 with o = 1 or 2 is a whole multiple of s / 2 between -2 and 2: an
-// fp16 number, never above the largest.  With c s + z = (c - o) s + (z + o s):
+// fp16 number, never above the largest.  (Where s is an odd multiple of fp16's
+// smallest step, half of it is not: s / 2, and a residual token's halved channel,
+// are then off by at most 2^-25.)  With c s + z = (c - o) s + (z + o s):
 //   score = 2 K' q + T,  T = q (z + s), one number a (key group, row), o = 1;
 //   out   = 2 V' p + sum_t p_t (z + o s)_t, one number a row; o = 1 for even, 2
 //           for odd tokens, so that both sums stay near the output's size (the

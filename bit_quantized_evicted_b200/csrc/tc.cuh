@@ -193,7 +193,8 @@ constexpr uint32_t kSuspendNs = 16384;
 // MMA every shared-memory access takes hundreds of cycles (looking at the abort
 // flag first doubled a wait that was over, to 300-400), and in kernels of many
 // roles the instruction caches are short.
-// up to n polls
+
+// Up to n polls of the barrier's phase: is it over?
 __device__ __forceinline__ uint32_t poll(uint64_t *bar, uint32_t parity, uint32_t n) {
     uint32_t done;
 #if MINIKV_ROLE_WAIT_LIMIT == 1   // the build whose waits give up at once: try_wait would suspend first, whatever its hint

@@ -38,7 +38,7 @@
 // only rows with others left are computed again, by slow_row (CUDA cores, visible
 // keys only).  8192 tokens, 32 heads, window 4096: 0.43 ms; with a NaN in a sink,
 // which all rows see, 0.95 (computed again row by row 66); with NaN padding behind
-// 8100 tokens 12, for the 28 rows a head that share a block with it.
+// 8100 tokens 12, for the 36 rows a head that share a block with it.
 #include <math.h>
 
 #include <mutex>

@@ -326,8 +326,14 @@ MINIKV_API int minikv_evict_pack_seq(const float *scores, const uint16_t *k, con
  * follows the actual per-sequence lengths).
  *   ws: minikv_workspace_size(MINIKV_OP_DECODE_ATTN, B, Hq, Hkv, cap + R + G, D, 0)
  *       bytes, ZERO-FILLED before its first use; every call leaves it ready for
- *       the next (its arrival counters return to zero).  Calls that share one
- *       ws must not overlap on the GPU.
+ *       the next of the same B and Hkv (its arrival counters return to zero;
+ *       those of another batch shape lie where this one keeps partial states,
+ *       so zero-fill it again first).  Calls that share one ws must not overlap
+ *       on the GPU.
+ * Precision: sums in fp32.  Long sums over packed values lose some bits (their
+ * codes are fp16 subnormals in the tensor cores): an error of up to 5e-4 of the
+ * output at several thousand tokens, where its rounding to fp16 is 2e-4.
+ * minikv_decode_attn_window and, behind a prefix, minikv_decode_attn_prefix do not.
  * Errors: INVALID_ARG (null, Hq % Hkv, ws too small), CAPACITY (a flush would
  * exceed cap), UNSUPPORTED (D != 128, Gv != D, G not 32/64/128, more than 4
  * query heads per KV head).
@@ -384,6 +390,10 @@ MINIKV_API int minikv_decode_attn_mass(minikv_cache *c, const uint16_t *q, const
  *       not read (up to the 32-token slices at the two ends of the hidden run).
  *       window >= n attends to every token, as minikv_decode_attn (the same but
  *       for rounding: this call's value sums are the more precise ones).
+ *       Numbers count the tokens that the cache holds.  After minikv_evict_pack
+ *       (or topk_evict) these are the kept ones, so the newest `window` of them
+ *       reach back further than `window` positions of the text: a model's own
+ *       window needs a cache that was not thinned out, or a smaller `window`.
  *   Nothing is dropped from the cache: a hidden token stays stored, and a flush
  *   packs the oldest residual tokens as usual.
  *   Uniform, ragged and device-state caches; ws as for minikv_decode_attn (the
