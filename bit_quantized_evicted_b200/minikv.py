@@ -150,7 +150,8 @@ def _own_ws(cache, name: str, need: int) -> torch.Tensor:
     """A call's default workspace, zero-filled when made and kept on the cache.  One that is too small for a later
     call (more query heads) is replaced but stays alive: a captured graph may have been given it."""
     if not _has_ws(cache, name, need):
-        cache.ws_replaced = [*getattr(cache, "ws_replaced", ()), getattr(cache, name, None)]
+        if hasattr(cache, name):
+            cache.ws_replaced = [*getattr(cache, "ws_replaced", ()), getattr(cache, name)]
         setattr(cache, name, torch.zeros(need, dtype=torch.uint8, device=cache.device))
     return getattr(cache, name)
 
